@@ -18,8 +18,10 @@ and row descriptors (tensors on the GPU; shapes as in the C header)::
     batch = peagle_build_draft_batch(out, acc, tok, start_pos, block_table,
                                      block_size, target_hidden, h_shared, mask_id)
 
-spec_verify_greedy / spec_verify_sample / spec_verify_mixed take a dense q
-instead; spec_verify_tree verifies draft trees; StepGraph captures a verify,
+spec_draft_sample_filtered and spec_verify_filtered(_lq) are the forms for
+requests with top-k, top-p and min-p, and peagle_append_kv writes the rebuilt
+batch's keys and values into the paged cache.  spec_verify_greedy /
+spec_verify_sample / spec_verify_mixed take a dense q instead; spec_verify_tree verifies draft trees; StepGraph captures a verify,
 build and acceptance-metrics step as one HIP graph.
 """
 from __future__ import annotations
@@ -44,13 +46,16 @@ __all__ = [
     "noalloc_scratch_bytes", "spec_verify_tree", "spec_verify_tree_lq", "spec_draft_sample",
     "spec_accept_metrics", "accept_metrics_buffer", "acceptance_summary", "StepGraph",
     "trace_begin", "trace_read", "trace_end",
+    "spec_draft_sample_filtered", "spec_verify_filtered", "spec_verify_filtered_lq",
+    "spec_filter_workspace_bytes", "peagle_append_kv",
     "DEVERR_DRAFT_TOKEN", "DEVERR_ACCEPT_COUNT", "DEVERR_BLOCK_TABLE",
 ]
 
-SV_F32, SV_BF16, SV_F16 = 0, 1, 2
+SV_F32, SV_BF16, SV_F16, SV_E4M3 = 0, 1, 2, 3
 PADDING_SLOT_ID = -1
 DEVERR_DRAFT_TOKEN, DEVERR_ACCEPT_COUNT, DEVERR_BLOCK_TABLE = 1, 2, 4
 DEVERR_ROW_INDEX, DEVERR_TEMPERATURE, DEVERR_TREE = 8, 16, 32
+DEVERR_FILTER, DEVERR_EMPTY_ROW, DEVERR_SLOT = 64, 128, 256
 MAX_B, MAX_K, MAX_V = 1 << 20, 63, 1 << 19      # SV_MAX_B, SV_MAX_K, SV_MAX_V
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -104,6 +109,19 @@ _SIGS = {
                                     ctypes.c_size_t, _p, _p]),
     "spec_verify_tree_mixed_early_exit": (_i, [_p, _i, _p, _p, _p, _p, _p, _i, _i, _i, _p, _p,
                                                _p, _p, ctypes.c_size_t, _p, _p]),
+    "spec_filter_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, _i]),
+    "spec_draft_sample_filtered": (_i, [_p, _i, ctypes.c_int64, ctypes.c_int64, _p, _p,
+                                        ctypes.c_float, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p,
+                                        ctypes.c_size_t, _p, _p]),
+    "spec_verify_filtered": (_i, [_p, _i, ctypes.c_int64, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i,
+                                  _p, _p, _p, _p, ctypes.c_size_t, _p, _p]),
+    "spec_verify_filtered_lq": (_i, [_p, _i, ctypes.c_int64, _p, ctypes.c_int64, ctypes.c_int64,
+                                     _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p,
+                                     ctypes.c_size_t, _p, _p]),
+    "peagle_append_kv": (_i, [_p, _p, _p, _i, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _p,
+                              _p, _p, _i, _i, ctypes.c_float, ctypes.c_int64, _i, _i, _i, _p, _p,
+                              _i, ctypes.c_int64, _i, ctypes.c_int64, ctypes.c_int64,
+                              ctypes.c_int64, _p, _p, _p, ctypes.c_int64, _p, _p]),
     "spec_accept_metrics_words": (ctypes.c_size_t, [_i]),
     "spec_accept_metrics": (_i, [_p, _i, _i, _p, _p, _p]),
     "sv_step_graph_create": (_i, [_p, _p]),
@@ -170,7 +188,7 @@ def _check(status: int, what: str):
 KERNEL_IDS = {"verify_greedy_rows": 0, "verify_sample_rows": 1, "verify_sample_draw": 2,
               "peagle_build": 3, "verify_greedy_accept": 4, "verify_sample_locate": 5,
               "draft_sample": 6, "verify_mixed_rows": 7, "accept_metrics": 8, "tree_rows": 9,
-              "tree_walk": 10}
+              "tree_walk": 10, "filter_rows": 12, "filtered_verify": 13, "append_kv": 14}
 
 
 def trace_begin(capacity: int, kernels=None):
@@ -689,6 +707,343 @@ def spec_verify_mixed_lq_early_exit(target_logits, drafter_logits, drafter_desc,
                       drafter_desc, draft_tokens, uniforms, None, temperatures, drafter_rows,
                       out_tokens, out_num_accepted, out_draft_target_prob,
                       want_draft_target_prob, workspace, device_error)
+
+
+# ---------------------------------------------------------------- filtered distributions
+def _rows(t: torch.Tensor, name: str, device=None, dtype=None) -> int:
+    """Checks logit rows [..., V] whose rows may be spaced wider than V (a
+    padded vocabulary); returns the elements between rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    V = t.shape[-1]
+    if V < 1:
+        raise ValueError(f"{name} must have at least one token per row")
+    if t.is_contiguous() or t.numel() == 0:
+        return V
+    step, rows = None, 1
+    for d in range(t.dim() - 2, -1, -1):           # the rows are evenly spaced in memory
+        if t.shape[d] == 1:
+            continue
+        if step is None:
+            step = t.stride(d)
+        elif t.stride(d) != step * rows:
+            raise ValueError(f"{name}'s rows must be evenly spaced")
+        rows *= t.shape[d]
+    if (t.stride(-1) != 1 and V > 1) or (step is not None and step < V):
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
+    return V if step is None else step
+
+
+def _settings(B, device, top_ks, top_ps, min_ps):
+    """Checks the per-sequence filter settings and returns their pointers."""
+    for t, name, dtype in ((top_ks, "top_ks", torch.int32), (top_ps, "top_ps", torch.float32),
+                           (min_ps, "min_ps", torch.float32)):
+        if t is not None:
+            _dev(t, name, dtype, (B,), device)
+    return _ptr(top_ks), _ptr(top_ps), _ptr(min_ps)
+
+
+def spec_filter_workspace_bytes(n_rows: int, V: int) -> int:
+    return int(require_library().spec_filter_workspace_bytes(int(n_rows), int(V)))
+
+
+def _filter_workspace(workspace, n_rows, V, device):
+    """The caller's workspace, or one of this call's own from torch's allocator
+    (which keeps it until the stream is past the call, also under capture)."""
+    if workspace is None:
+        return torch.empty(max(16, spec_filter_workspace_bytes(n_rows, V)), dtype=torch.uint8,
+                           device=device)
+    return _dev(workspace, "workspace", device=device)
+
+
+def _on(device):
+    """The guard under which a call launches: its tensors' device is current."""
+    return torch.cuda.device(device)
+
+
+def spec_draft_sample_filtered(drafter_logits: torch.Tensor, K: int, temperature: float = 1.0,
+                               top_ks: Optional[torch.Tensor] = None,
+                               top_ps: Optional[torch.Tensor] = None,
+                               min_ps: Optional[torch.Tensor] = None,
+                               uniforms: Optional[torch.Tensor] = None,
+                               row_index: Optional[torch.Tensor] = None,
+                               temperatures: Optional[torch.Tensor] = None,
+                               out_draft_tokens: Optional[torch.Tensor] = None,
+                               out_draft_probs: Optional[torch.Tensor] = None,
+                               want_draft_probs: bool = False,
+                               out_filter_rows: Optional[torch.Tensor] = None,
+                               want_filter_rows: bool = False,
+                               workspace: Optional[torch.Tensor] = None,
+                               device_error: Optional[torch.Tensor] = None):
+    """Sample logit rows under temperature, top-k, top-p and min-p; see
+    spec_draft_sample_filtered in include/spec_verify.h.
+
+    drafter_logits [n_rows, V] float32/bfloat16 (rows may be spaced wider than
+    V); B is taken from row_index ([B, K]) when given, else n_rows // K.  K = 1
+    samples one token per row (a decode step without drafts).  top_ks [B] int32
+    (0 = off), top_ps [B] and min_ps [B] float32 (1 and 0 = off) are per
+    sequence, None = off for all; temperatures [B] overrides temperature.
+
+    Returns (draft_tokens [B, K] int32, draft_probs [B, K, V] fp32 or None,
+    filter_rows [B, K, 8] int32 holding sv_filter_row or None).
+    """
+    lib = require_library()
+    if drafter_logits.dim() != 2:
+        raise ValueError("drafter_logits must be [n_rows, V]")
+    n_rows, V = drafter_logits.shape
+    dev = drafter_logits.device
+    stride = _rows(drafter_logits, "drafter_logits")
+    if row_index is not None:
+        if row_index.dim() != 2 or row_index.shape[1] != K:
+            raise ValueError("row_index must be [B, K]")
+        B = row_index.shape[0]
+        _dev(row_index, "row_index", torch.int32, (B, K), dev)
+    else:
+        if K < 1 or n_rows % K:
+            raise ValueError("without row_index, n_rows must be a multiple of K")
+        B = n_rows // K
+    if uniforms is not None:
+        _dev(uniforms, "uniforms", torch.float32, (B, K), dev)
+    if temperatures is not None:
+        _dev(temperatures, "temperatures", torch.float32, (B,), dev)
+    settings = _settings(B, dev, top_ks, top_ps, min_ps)
+    out_draft_tokens = torch.empty((B, K), dtype=torch.int32, device=dev) \
+        if out_draft_tokens is None else _dev(out_draft_tokens, "out_draft_tokens", torch.int32,
+                                              (B, K), dev)
+    if out_draft_probs is None and want_draft_probs:
+        out_draft_probs = torch.empty((B, K, V), dtype=torch.float32, device=dev)
+    if out_draft_probs is not None:
+        _dev(out_draft_probs, "out_draft_probs", torch.float32, (B, K, V), dev)
+    if out_filter_rows is None and want_filter_rows:
+        out_filter_rows = torch.empty((B, K, 8), dtype=torch.int32, device=dev)
+    if out_filter_rows is not None:
+        _dev(out_filter_rows, "out_filter_rows", torch.int32, (B, K, 8), dev)
+    if device_error is not None:
+        _dev(device_error, "device_error", torch.int32, (1,), dev)
+    workspace = _filter_workspace(workspace, B * K, V, dev)
+    with _on(dev):
+        st = lib.spec_draft_sample_filtered(
+            _ptr(drafter_logits), _DTYPES[drafter_logits.dtype], n_rows, stride, _ptr(row_index),
+            _ptr(uniforms), float(temperature), _ptr(temperatures), *settings, B, K, V,
+            _ptr(out_draft_tokens), _ptr(out_draft_probs), _ptr(out_filter_rows), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(device_error), _stream(dev))
+    _check(st, "spec_draft_sample_filtered")
+    return out_draft_tokens, out_draft_probs, out_filter_rows
+
+
+def _verify_filtered(name, target_logits, q_args, draft_tokens, uniforms, temperatures, top_ks,
+                     top_ps, min_ps, out_tokens, out_num_accepted, out_draft_target_prob,
+                     want_draft_target_prob, workspace, device_error):
+    """spec_verify_filtered and _lq: q_args(B, K, V, device) checks the q
+    arguments and gives what the library takes for them."""
+    lib = require_library()
+    if target_logits.dim() != 3:
+        raise ValueError("target_logits must be [B, K+1, V]")
+    B, K1, V = target_logits.shape
+    K = K1 - 1
+    dev = target_logits.device
+    stride = _rows(target_logits, "target_logits")
+    q = q_args(B, K, V, dev)
+    _dev(draft_tokens, "draft_tokens", torch.int32, (B, K), dev)
+    _dev(uniforms, "uniforms", torch.float32, (B, K + 1), dev)
+    _dev(temperatures, "temperatures", torch.float32, (B,), dev)
+    settings = _settings(B, dev, top_ks, top_ps, min_ps)
+    out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev) if out_tokens is None \
+        else _dev(out_tokens, "out_tokens", torch.int32, (B, K + 1), dev)
+    out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev) if out_num_accepted is None \
+        else _dev(out_num_accepted, "out_num_accepted", torch.int32, (B,), dev)
+    if out_draft_target_prob is None and want_draft_target_prob:
+        out_draft_target_prob = torch.empty((B, K), dtype=torch.float32, device=dev)
+    if out_draft_target_prob is not None:
+        _dev(out_draft_target_prob, "out_draft_target_prob", torch.float32, (B, K), dev)
+    if device_error is not None:
+        _dev(device_error, "device_error", torch.int32, (1,), dev)
+    workspace = _filter_workspace(workspace, B * (K + 1), V, dev)
+    with _on(dev):
+        st = getattr(lib, name)(
+            _ptr(target_logits), _DTYPES[target_logits.dtype], stride, *q, _ptr(draft_tokens),
+            _ptr(uniforms), _ptr(temperatures), *settings, B, K, V, _ptr(out_tokens),
+            _ptr(out_num_accepted), _ptr(out_draft_target_prob), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(device_error), _stream(dev))
+    _check(st, name)
+    return out_tokens, out_num_accepted, out_draft_target_prob
+
+
+def spec_verify_filtered(target_logits: torch.Tensor, draft_probs: torch.Tensor,
+                         draft_tokens: torch.Tensor, uniforms: torch.Tensor,
+                         temperatures: torch.Tensor, top_ks: Optional[torch.Tensor] = None,
+                         top_ps: Optional[torch.Tensor] = None,
+                         min_ps: Optional[torch.Tensor] = None,
+                         out_tokens: Optional[torch.Tensor] = None,
+                         out_num_accepted: Optional[torch.Tensor] = None,
+                         out_draft_target_prob: Optional[torch.Tensor] = None,
+                         want_draft_target_prob: bool = False,
+                         workspace: Optional[torch.Tensor] = None,
+                         device_error: Optional[torch.Tensor] = None):
+    """Verify against the target's filtered distributions (per-sequence
+    temperature, 0 = greedy, top-k, top-p and min-p); see spec_verify_filtered
+    in include/spec_verify.h.  target_logits [B, K+1, V] (rows may be spaced
+    wider than V), draft_probs [B, K, V] float32; settings as for
+    spec_draft_sample_filtered.
+
+    Returns (out_tokens [B, K+1], num_accepted [B], draft_target_prob or None).
+    """
+    def q_args(B, K, V, dev):
+        _dev(draft_probs, "draft_probs", torch.float32, (B, K, V), dev)
+        return (_ptr(draft_probs),)
+
+    return _verify_filtered("spec_verify_filtered", target_logits, q_args, draft_tokens, uniforms,
+                            temperatures, top_ks, top_ps, min_ps, out_tokens, out_num_accepted,
+                            out_draft_target_prob, want_draft_target_prob, workspace, device_error)
+
+
+def spec_verify_filtered_lq(target_logits: torch.Tensor, drafter_logits: torch.Tensor,
+                            filter_rows: torch.Tensor, draft_tokens: torch.Tensor,
+                            uniforms: torch.Tensor, temperatures: torch.Tensor,
+                            top_ks: Optional[torch.Tensor] = None,
+                            top_ps: Optional[torch.Tensor] = None,
+                            min_ps: Optional[torch.Tensor] = None,
+                            drafter_rows: Optional[torch.Tensor] = None,
+                            out_tokens: Optional[torch.Tensor] = None,
+                            out_num_accepted: Optional[torch.Tensor] = None,
+                            out_draft_target_prob: Optional[torch.Tensor] = None,
+                            want_draft_target_prob: bool = False,
+                            workspace: Optional[torch.Tensor] = None,
+                            device_error: Optional[torch.Tensor] = None):
+    """spec_verify_filtered with q from the drafter's logits [n_rows, V] and the
+    filter rows ([B, K, 8] int32) of spec_draft_sample_filtered; see
+    spec_verify_filtered_lq in include/spec_verify.h."""
+    def q_args(B, K, V, dev):
+        if drafter_logits.dim() != 2 or drafter_logits.shape[1] != V:
+            raise ValueError("drafter_logits must be [n_rows, V]")
+        d_stride = _rows(drafter_logits, "drafter_logits", dev, target_logits.dtype)
+        _dev(filter_rows, "filter_rows", torch.int32, (B, K, 8), dev)
+        if drafter_rows is not None:
+            _dev(drafter_rows, "drafter_rows", torch.int32, (B, K), dev)
+        return (_ptr(drafter_logits), drafter_logits.shape[0], d_stride, _ptr(drafter_rows),
+                _ptr(filter_rows))
+
+    return _verify_filtered("spec_verify_filtered_lq", target_logits, q_args, draft_tokens,
+                            uniforms, temperatures, top_ks, top_ps, min_ps, out_tokens,
+                            out_num_accepted, out_draft_target_prob, want_draft_target_prob,
+                            workspace, device_error)
+
+
+# ---------------------------------------------------------------- paged cache
+def _heads(t: torch.Tensor, name: str, R, D, dtype, device):
+    """Checks [R, heads, D] rows with dense heads; returns (heads, elements
+    between rows)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != R or t.shape[2] != D:
+        raise ValueError(f"{name} must be [{R}, heads, {D}], got {tuple(t.shape)}")
+    H = t.shape[1]
+    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}'s heads must be dense in each row")
+    stride = t.stride(0) if R > 1 else H * D
+    if stride < H * D and t.numel():
+        raise ValueError(f"{name}'s rows must not overlap")
+    return H, max(stride, H * D)
+
+
+def peagle_append_kv(key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                     slot_mapping: torch.Tensor, key_cache: torch.Tensor,
+                     value_cache: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
+                     interleaved: bool = False, rotary_scale: float = 1.0,
+                     query: Optional[torch.Tensor] = None,
+                     out_query: Optional[torch.Tensor] = None,
+                     k_scales: Optional[torch.Tensor] = None,
+                     v_scales: Optional[torch.Tensor] = None,
+                     device_error: Optional[torch.Tensor] = None):
+    """Append keys and values to a paged cache, rotating keys (and queries) by
+    their positions; see peagle_append_kv in include/spec_verify.h.
+
+    key, value [R, kv_heads, D] and the optional query [R, q_heads, D] in
+    bfloat16, float16 or float32 (rows may be views into one projection);
+    positions and slot_mapping [R] int64 as peagle_build_draft_batch writes them
+    (slot -1: nothing is written); inv_freq [rotary_dim / 2] float32, None for no
+    rotation; caches [num_blocks, block_size, kv_heads, D] of the same type or
+    float8_e4m3fn, the last dimension dense, the others with any strides that
+    both caches share; k_scales, v_scales [kv_heads] float32 for e4m3 caches.
+
+    Returns the rotated queries (out_query, which may be query itself) or None.
+    """
+    lib = require_library()
+    if not isinstance(key, torch.Tensor) or key.dim() != 3:
+        raise ValueError("key must be [R, kv_heads, head_dim]")
+    R, Hkv, D = key.shape
+    dev, dtype = key.device, key.dtype
+    if dtype not in _DTYPES:
+        raise TypeError("keys must be bfloat16, float16 or float32")
+    _, ks = _heads(key, "key", R, D, dtype, dev)
+    Hv, vs = _heads(value, "value", R, D, dtype, dev)
+    if Hv != Hkv:
+        raise ValueError(f"value must have {Hkv} heads, got {Hv}")
+    _dev(positions, "positions", torch.int64, (R,), dev)
+    _dev(slot_mapping, "slot_mapping", torch.int64, (R,), dev)
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rotary_dim / 2]")
+        _dev(inv_freq, "inv_freq", torch.float32, device=dev)
+        rot = 2 * inv_freq.shape[0]
+    if key_cache.dim() != 4 or key_cache.shape[2:] != (Hkv, D):
+        raise ValueError(f"key_cache must be [num_blocks, block_size, {Hkv}, {D}]")
+    if value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache must have one shape")
+    for t, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+        if t.dtype is not dtype and t.dtype is not torch.float8_e4m3fn:
+            raise TypeError(f"{name} must be {dtype} or float8_e4m3fn")
+    if key_cache.dtype is not value_cache.dtype or key_cache.stride() != value_cache.stride():
+        raise ValueError("key_cache and value_cache must have one type and one layout")
+    if D > 1 and key_cache.stride(3) != 1:
+        raise ValueError("the caches' last dimension must be dense")
+    fp8 = key_cache.dtype is torch.float8_e4m3fn
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t is not None:
+            if not fp8:
+                raise ValueError(f"{name} are for float8_e4m3fn caches")
+            _dev(t, name, torch.float32, (Hkv,), dev)
+    Hq = qs = oqs = 0
+    if query is not None:
+        if query.dim() != 3:
+            raise ValueError("query must be [R, q_heads, head_dim]")
+        Hq, qs = _heads(query, "query", R, D, dtype, dev)
+        if out_query is None:
+            out_query = torch.empty((R, Hq, D), dtype=dtype, device=dev)
+        Ho, oqs = _heads(out_query, "out_query", R, D, dtype, dev)
+        if Ho != Hq:
+            raise ValueError(f"out_query must have {Hq} heads, got {Ho}")
+    elif out_query is not None:
+        raise ValueError("out_query without query")
+    if device_error is not None:
+        _dev(device_error, "device_error", torch.int32, (1,), dev)
+    nb, bs = key_cache.shape[:2]
+    with _on(dev):
+        st = lib.peagle_append_kv(
+            _ptr(query), _ptr(key), _ptr(value), _DTYPES[dtype], qs, ks, vs, _ptr(positions),
+            _ptr(slot_mapping), _ptr(inv_freq), rot, 1 if interleaved else 0, float(rotary_scale),
+            R, Hq, Hkv, D, _ptr(key_cache), _ptr(value_cache), SV_E4M3 if fp8 else _DTYPES[dtype],
+            nb, bs, key_cache.stride(0), key_cache.stride(1), key_cache.stride(2),
+            _ptr(k_scales), _ptr(v_scales), _ptr(out_query), oqs, _ptr(device_error), _stream(dev))
+    _check(st, "peagle_append_kv")
+    return out_query
 
 
 # ---------------------------------------------------------------- draft trees

@@ -55,6 +55,7 @@ namespace {
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 constexpr long kMaxB = SV_MAX_B;    // sequences per call
+constexpr long kMaxRowStride = 1L << 31;   // elements between logit rows (filtered calls)
 
 sv_status check_verify_shape(int B, int K, int V) {
   if (B < 0 || B > kMaxB || K < 0 || K > SV_MAX_K || V < 1 || V > SV_MAX_V) return SV_ERR_SHAPE;
@@ -93,6 +94,9 @@ SV_API const char* sv_kernel_name(int kernel_id) {
     case SV_KERNEL_ACCEPT_METRICS: return "accept_metrics";
     case SV_KERNEL_TREE_ROWS: return "tree_rows";
     case SV_KERNEL_TREE_WALK: return "tree_walk";
+    case SV_KERNEL_FILTER_ROWS: return "filter_rows";
+    case SV_KERNEL_FILTERED_VERIFY: return "filtered_verify";
+    case SV_KERNEL_APPEND_KV: return "append_kv";
     default: return "unknown";
   }
 }
@@ -374,6 +378,67 @@ sv_status tree_lq(const void* target_logits, int logits_dtype, const void* draft
   return sv::launch_tree(L, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
+// spec_verify_filtered (dense q) and spec_verify_filtered_lq (`lq`: q from the
+// drafter's logits and filter rows).
+sv_status verify_filtered(const void* target_logits, int logits_dtype, int64_t row_stride,
+                          const float* draft_probs, const void* drafter_logits,
+                          int64_t n_drafter_rows, int64_t drafter_row_stride,
+                          const int32_t* drafter_rows, const sv_filter_row* filter_rows, bool lq,
+                          const int32_t* draft_tokens, const float* uniforms,
+                          const float* temperatures, const int32_t* top_ks, const float* top_ps,
+                          const float* min_ps, int B, int K, int V, int32_t* out_tokens,
+                          int32_t* out_num_accepted, float* out_draft_target_prob, void* workspace,
+                          size_t workspace_bytes, int32_t* device_error, void* stream) {
+  sv_status st = check_verify_shape(B, K, V);
+  if (st != SV_OK) return st;
+  if (row_stride < V || row_stride > kMaxRowStride) return SV_ERR_SHAPE;
+  if (lq && K > 0 &&
+      (n_drafter_rows < 0 || n_drafter_rows > 0x7fffffffL || drafter_row_stride < V ||
+       drafter_row_stride > kMaxRowStride || (!drafter_rows && n_drafter_rows < (int64_t)B * K)))
+    return SV_ERR_SHAPE;
+  if (logits_dtype != SV_F32 && logits_dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (B == 0) return SV_OK;
+  if (!target_logits || !uniforms || !temperatures || !out_tokens || !out_num_accepted)
+    return SV_ERR_NULL;
+  if (K > 0 && (!draft_tokens || (lq ? !drafter_logits || !filter_rows : !draft_probs)))
+    return SV_ERR_NULL;
+  if (!workspace || workspace_bytes < filter_workspace_bytes((long)B * (K + 1), V))
+    return SV_ERR_WORKSPACE;
+  const size_t esz = logits_dtype == SV_BF16 ? 2 : 4;
+  if (!aligned(target_logits, esz) || !aligned(draft_probs, 4) || !aligned(drafter_logits, esz) ||
+      !aligned(drafter_rows, 4) || !aligned(filter_rows, 16) || !aligned(draft_tokens, 4) ||
+      !aligned(uniforms, 4) || !aligned(temperatures, 4) || !aligned(top_ks, 4) ||
+      !aligned(top_ps, 4) || !aligned(min_ps, 4) || !aligned(out_tokens, 4) ||
+      !aligned(out_num_accepted, 4) || !aligned(out_draft_target_prob, 4) ||
+      !aligned(workspace, 16) || !aligned(device_error, 4))
+    return SV_ERR_ALIGN;
+  FilteredVerifyLaunch L{};
+  L.logits = target_logits;
+  L.row_stride = (long)row_stride;
+  L.draft_probs = draft_probs;
+  L.lq = lq ? 1 : 0;
+  L.dlogits = drafter_logits;
+  L.d_stride = (long)drafter_row_stride;
+  L.d_rows = (long)n_drafter_rows;
+  L.drows = drafter_rows;
+  L.ddesc = filter_rows;
+  L.draft_tokens = draft_tokens;
+  L.uniforms = uniforms;
+  L.temperatures = temperatures;
+  L.top_ks = top_ks;
+  L.top_ps = top_ps;
+  L.min_ps = min_ps;
+  L.B = B; L.K = K; L.V = V;
+  L.bf16 = logits_dtype == SV_BF16;
+  L.out_tokens = out_tokens;
+  L.out_num_accepted = out_num_accepted;
+  L.out_p = out_draft_target_prob;
+  L.workspace = workspace;
+  L.device_error = device_error;
+  return launch_filtered_verify(L, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK
+                                                                                   : SV_ERR_HIP;
+}
+
 }  // namespace sv
 
 extern "C" {
@@ -602,6 +667,155 @@ SV_API sv_status spec_draft_sample(const void* drafter_logits, int logits_dtype,
   L.out_desc = out_row_desc;
   L.device_error = device_error;
   return sv::launch_draft(L, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+SV_API size_t spec_filter_workspace_bytes(int64_t n_rows, int V) {
+  if (n_rows < 1 || n_rows > kMaxB * (SV_MAX_K + 1L) || V < 1 || V > SV_MAX_V) return 0;
+  return sv::filter_workspace_bytes((long)n_rows, V);
+}
+
+SV_API sv_status spec_draft_sample_filtered(
+    const void* drafter_logits, int logits_dtype, int64_t n_rows, int64_t row_stride,
+    const int32_t* row_index, const float* uniforms, float temperature,
+    const float* temperatures, const int32_t* top_ks, const float* top_ps, const float* min_ps,
+    int B, int K, int V, int32_t* out_draft_tokens, float* out_draft_probs,
+    sv_filter_row* out_filter_rows, void* workspace, size_t workspace_bytes,
+    int32_t* device_error, void* stream) {
+  if (B < 0 || B > kMaxB || K < 1 || K > SV_MAX_K || V < 1 || V > SV_MAX_V || n_rows < 0 ||
+      n_rows > 0x7fffffffL || row_stride < V || row_stride > kMaxRowStride)
+    return SV_ERR_SHAPE;
+  if (!row_index && n_rows < (int64_t)B * K) return SV_ERR_SHAPE;
+  if (logits_dtype != SV_F32 && logits_dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (!(temperature >= 0.0f && isfinite(temperature))) return SV_ERR_VALUE;
+  if (temperature > 0.0f && !isfinite((float)(1.4426950408889634 / (double)temperature)))
+    return SV_ERR_VALUE;
+  if (B == 0) return SV_OK;
+  if (!drafter_logits || !out_draft_tokens) return SV_ERR_NULL;
+  if (!uniforms && (temperature != 0.0f || temperatures)) return SV_ERR_NULL;
+  if (!workspace || workspace_bytes < sv::filter_workspace_bytes((long)B * K, V))
+    return SV_ERR_WORKSPACE;
+  const size_t esz = logits_dtype == SV_BF16 ? 2 : 4;
+  if (!aligned(drafter_logits, esz) || !aligned(out_draft_tokens, 4) || !aligned(row_index, 4) ||
+      !aligned(uniforms, 4) || !aligned(temperatures, 4) || !aligned(top_ks, 4) ||
+      !aligned(top_ps, 4) || !aligned(min_ps, 4) || !aligned(out_draft_probs, 4) ||
+      !aligned(out_filter_rows, 16) || !aligned(workspace, 16) || !aligned(device_error, 4))
+    return SV_ERR_ALIGN;
+  sv::FilterLaunch L{};
+  L.logits = drafter_logits;
+  L.row_stride = (long)row_stride;
+  L.row_index = row_index;
+  L.n_rows = (long)n_rows;
+  L.uniforms = uniforms;
+  L.temperatures = temperatures;
+  L.temperature = temperature;
+  L.top_ks = top_ks;
+  L.top_ps = top_ps;
+  L.min_ps = min_ps;
+  L.B = B; L.per_seq = K; L.V = V;
+  L.bf16 = logits_dtype == SV_BF16;
+  L.out_tokens = out_draft_tokens;
+  L.out_probs = out_draft_probs;
+  L.out_rows = out_filter_rows;
+  L.device_error = device_error;
+  return sv::launch_filter_rows(L, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK
+                                                                                   : SV_ERR_HIP;
+}
+
+SV_API sv_status spec_verify_filtered(
+    const void* target_logits, int logits_dtype, int64_t row_stride, const float* draft_probs,
+    const int32_t* draft_tokens, const float* uniforms, const float* temperatures,
+    const int32_t* top_ks, const float* top_ps, const float* min_ps, int B, int K, int V,
+    int32_t* out_tokens, int32_t* out_num_accepted, float* out_draft_target_prob,
+    void* workspace, size_t workspace_bytes, int32_t* device_error, void* stream) {
+  return sv::verify_filtered(target_logits, logits_dtype, row_stride, draft_probs, nullptr, 0, 0,
+                             nullptr, nullptr, false, draft_tokens, uniforms, temperatures, top_ks,
+                             top_ps, min_ps, B, K, V, out_tokens, out_num_accepted,
+                             out_draft_target_prob, workspace, workspace_bytes, device_error,
+                             stream);
+}
+
+SV_API sv_status spec_verify_filtered_lq(
+    const void* target_logits, int logits_dtype, int64_t row_stride, const void* drafter_logits,
+    int64_t n_drafter_rows, int64_t drafter_row_stride, const int32_t* drafter_rows,
+    const sv_filter_row* filter_rows, const int32_t* draft_tokens, const float* uniforms,
+    const float* temperatures, const int32_t* top_ks, const float* top_ps, const float* min_ps,
+    int B, int K, int V, int32_t* out_tokens, int32_t* out_num_accepted,
+    float* out_draft_target_prob, void* workspace, size_t workspace_bytes,
+    int32_t* device_error, void* stream) {
+  return sv::verify_filtered(target_logits, logits_dtype, row_stride, nullptr, drafter_logits,
+                             n_drafter_rows, drafter_row_stride, drafter_rows, filter_rows, true,
+                             draft_tokens, uniforms, temperatures, top_ks, top_ps, min_ps, B, K, V,
+                             out_tokens, out_num_accepted, out_draft_target_prob, workspace,
+                             workspace_bytes, device_error, stream);
+}
+
+SV_API sv_status peagle_append_kv(
+    const void* query, const void* key, const void* value, int dtype, int64_t query_stride,
+    int64_t key_stride, int64_t value_stride, const int64_t* positions,
+    const int64_t* slot_mapping, const float* inv_freq, int rotary_dim, int interleaved,
+    float rotary_scale, int64_t R, int q_heads, int kv_heads, int head_dim, void* key_cache,
+    void* value_cache, int cache_dtype, int64_t num_blocks, int block_size,
+    int64_t block_stride, int64_t slot_stride, int64_t head_stride, const float* k_scales,
+    const float* v_scales, void* out_query, int64_t out_query_stride, int32_t* device_error,
+    void* stream) {
+  if (R < 0 || R > 0x7fffffffL || q_heads < 0 || q_heads > SV_MAX_HEADS || kv_heads < 1 ||
+      kv_heads > SV_MAX_HEADS || head_dim < 1 || head_dim > SV_MAX_HEAD_DIM || rotary_dim < 0 ||
+      rotary_dim > head_dim || rotary_dim % 2 || num_blocks < 1 || block_size < 1)
+    return SV_ERR_SHAPE;
+  if (num_blocks > (int64_t)1 << 40 || key_stride < (int64_t)kv_heads * head_dim ||
+      value_stride < (int64_t)kv_heads * head_dim || block_stride < 0 || slot_stride < 0 ||
+      head_stride < 0)
+    return SV_ERR_SHAPE;
+  if (q_heads > 0 && (query_stride < (int64_t)q_heads * head_dim ||
+                      out_query_stride < (int64_t)q_heads * head_dim))
+    return SV_ERR_SHAPE;
+  if (dtype != SV_F32 && dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
+  if (cache_dtype != dtype && cache_dtype != SV_E4M3) return SV_ERR_DTYPE;
+  if (!isfinite(rotary_scale) || (cache_dtype != SV_E4M3 && (k_scales || v_scales)))
+    return SV_ERR_VALUE;
+  if (R == 0) return SV_OK;
+  if (!key || !value || !positions || !slot_mapping || !key_cache || !value_cache ||
+      (rotary_dim > 0 && !inv_freq) || (q_heads > 0 && (!query || !out_query)))
+    return SV_ERR_NULL;
+  const size_t esz = dtype == SV_F32 ? 4 : 2, csz = cache_dtype == SV_E4M3 ? 1 : esz;
+  if (!aligned(key, esz) || !aligned(value, esz) || !aligned(positions, 8) ||
+      !aligned(slot_mapping, 8) || !aligned(key_cache, csz) || !aligned(value_cache, csz) ||
+      !aligned(inv_freq, 4) || !aligned(k_scales, 4) || !aligned(v_scales, 4) ||
+      !aligned(device_error, 4) ||
+      (q_heads > 0 && (!aligned(query, esz) || !aligned(out_query, esz))))
+    return SV_ERR_ALIGN;
+  sv::AppendLaunch L{};
+  L.query = query;
+  L.key = key;
+  L.value = value;
+  L.dtype = dtype;
+  L.q_stride = query_stride;
+  L.k_stride = key_stride;
+  L.v_stride = value_stride;
+  L.out_q_stride = out_query_stride;
+  L.positions = positions;
+  L.slots = slot_mapping;
+  L.inv_freq = inv_freq;
+  L.rot = rotary_dim;
+  L.interleaved = interleaved != 0;
+  L.rotary_scale = rotary_scale;
+  L.R = (long)R;
+  L.q_heads = q_heads;
+  L.kv_heads = kv_heads;
+  L.head_dim = head_dim;
+  L.key_cache = key_cache;
+  L.value_cache = value_cache;
+  L.fp8 = cache_dtype == SV_E4M3;
+  L.num_slots = (long)num_blocks * block_size;
+  L.block_size = block_size;
+  L.block_stride = block_stride;
+  L.slot_stride = slot_stride;
+  L.head_stride = head_stride;
+  L.k_scales = k_scales;
+  L.v_scales = v_scales;
+  L.out_query = out_query;
+  L.device_error = device_error;
+  return sv::launch_append(L, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
 SV_API sv_status spec_verify_tree(const void* target_logits, int logits_dtype,

@@ -1,0 +1,165 @@
+// Filtered distributions (temperature, top-k, top-p, min-p) of logit rows, for
+// the filtered sampler and the filtered verify (gfx950, wave64).
+//
+// A row z[V] at temperature T has weights w(x) = 2^((z(x) - m) c), m = max z,
+// c = log2(e) / T.  Its tokens are ordered by logit, the largest first, equal
+// logits by index; -inf and NaN logits are never kept.  Every filter keeps a
+// prefix of that order, so a kept set is described by its last token alone:
+// token x is kept iff z(x) > z_last, or z(x) = z_last and x <= last.
+//
+// Weights and their sums are fp64: top-p cuts between two neighbouring
+// running sums, which differ by one token's share (1e-5 of the total and less
+// in a flat row of 150k tokens) and which fp32 exponentials (1e-7 each) do not
+// tell apart reliably.
+#pragma once
+
+#include <math.h>
+
+#include "../../include/spec_verify.h"
+#include "sv_device.h"
+#include "sv_rowstats.h"
+
+namespace sv {
+
+// ---------------------------------------------------------------- keys
+// Unsigned key of a logit that grows with it: -0 and +0 share one, NaN counts
+// as -inf.  Every finite logit's key is greater than kKeyNegInf.
+constexpr uint32_t kKeyNegInf = 0x007fffffu;
+__device__ __forceinline__ float clean_logit(float z) {
+  return z > -INFINITY ? z + 0.f : -INFINITY;
+}
+__device__ __forceinline__ uint32_t logit_key(float z) {       // z cleaned
+  const uint32_t b = __float_as_uint(z);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+
+// ---------------------------------------------------------------- weights
+// 2^x in fp64 for x <= 0: x = n + f, |f| <= 1/2, the exponential series of
+// f ln 2 up to its 12th power (the 13th is below 2e-16).
+__device__ __forceinline__ double exp2_f64(double x) {
+  x = fmax(x, -1100.0);                     // 0 after the scaling; also -inf and NaN
+  const double n = rint(x);
+  const double f = x - n;
+  double p = 2.5678435993488196e-11;        // (ln 2)^k / k!, k = 12 .. 0
+  p = fma(p, f, 4.4455382718708101e-10);
+  p = fma(p, f, 7.0549116208011209e-09);
+  p = fma(p, f, 1.0178086009239696e-07);
+  p = fma(p, f, 1.3215486790144305e-06);
+  p = fma(p, f, 1.5252733804059838e-05);
+  p = fma(p, f, 1.5403530393381606e-04);
+  p = fma(p, f, 1.3333558146428441e-03);
+  p = fma(p, f, 9.6181291076284769e-03);
+  p = fma(p, f, 5.5504108664821576e-02);
+  p = fma(p, f, 2.4022650695910069e-01);
+  p = fma(p, f, 6.9314718055994529e-01);
+  p = fma(p, f, 1.0);
+  return ldexp(p, (int)n);
+}
+
+// The weight of logit z in a row of maximum m: 1 at the maximum (also where
+// that is +inf), 0 at -inf.
+__device__ __forceinline__ double weight(float z, float m, double c) {
+  if (z == m) return 1.0;
+  return z > -INFINITY ? exp2_f64(((double)z - (double)m) * c) : 0.0;
+}
+
+// Whether a filter row keeps token x of logit z (cleaned).
+__device__ __forceinline__ bool row_keeps(const sv_filter_row& f, float z, long x) {
+  return z > f.min_kept || (z == f.min_kept && x <= (long)f.last);
+}
+// The probability a filter row gives token x of logit z.
+__device__ __forceinline__ double row_prob(const sv_filter_row& f, float z, long x) {
+  z = clean_logit(z);
+  return row_keeps(f, z, x) ? weight(z, f.max, f.scale) * f.inv_sum : 0.0;
+}
+
+// ---------------------------------------------------------------- settings
+struct FilterSettings {
+  double c;      // log2(e) / T; 0: greedy
+  int k;         // 1 .. V (V: off)
+  double p;      // >= 1: off
+  double mp;     // <= 0: off
+  bool off;      // no filter at all
+};
+
+// The settings of sequence b.  Bad values are flagged and switched off (a bad
+// temperature is greedy, as everywhere else).
+__device__ __forceinline__ FilterSettings filter_settings(const float* temperatures,
+                                                          float temperature, const int32_t* top_ks,
+                                                          const float* top_ps, const float* min_ps,
+                                                          int b, int V, int& errors) {
+  FilterSettings s;
+  bool bad;
+  const float T = temperatures ? temperatures[b] : temperature;
+  const float c32 = seq_scale(T, bad);
+  if (bad) errors |= SV_DEVERR_TEMPERATURE;
+  s.c = c32 == 0.f ? 0.0 : 1.4426950408889634 / (double)T;
+  int k = top_ks ? top_ks[b] : 0;
+  float p = top_ps ? top_ps[b] : 1.f;
+  float mp = min_ps ? min_ps[b] : 0.f;
+  if (k < 0) { errors |= SV_DEVERR_FILTER; k = 0; }
+  if (!(p > 0.f && p <= 1.f)) { errors |= SV_DEVERR_FILTER; p = 1.f; }
+  if (!(mp >= 0.f && mp <= 1.f)) { errors |= SV_DEVERR_FILTER; mp = 0.f; }
+  if (c32 == 0.f) { k = 1; p = 1.f; mp = 0.f; }
+  s.k = k == 0 || k > V ? V : k;
+  s.p = (double)p;
+  s.mp = (double)mp;
+  s.off = s.k == V && s.p >= 1.0 && s.mp <= 0.0 && c32 != 0.f;
+  return s;
+}
+
+// ---------------------------------------------------------------- workgroup reductions
+// Each gives every thread the result; sm holds one entry per wave.
+template <int THREADS, typename T, typename OP>
+__device__ __forceinline__ T block_reduce(T x, T* sm, OP op) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) x = op(x, __shfl_xor(x, off));
+  __syncthreads();                      // sm may still be read from before
+  if (lane_id() == 0) sm[threadIdx.x / kWave] = x;
+  __syncthreads();
+  x = sm[0];
+#pragma unroll
+  for (int i = 1; i < THREADS / kWave; ++i) x = op(x, sm[i]);
+  return x;
+}
+struct OpAdd { template <typename T> __device__ T operator()(T a, T b) const { return a + b; } };
+struct OpMax { template <typename T> __device__ T operator()(T a, T b) const { return a > b ? a : b; } };
+struct OpMin { template <typename T> __device__ T operator()(T a, T b) const { return a < b ? a : b; } };
+
+// ---------------------------------------------------------------- loads
+// Eight consecutive logits from element e on, whatever the row's alignment: a
+// row of odd length, or one inside a padded buffer, starts at any multiple of
+// its element size, and gfx950 loads 16 bytes from any such address.
+struct __attribute__((packed, aligned(2))) OctBf16 { u32x4 w; };
+struct __attribute__((packed, aligned(4))) OctF32 { u32x4 a, b; };
+__device__ __forceinline__ void load8(const uint16_t* p, float z[8]) {
+  const u32x4 w = reinterpret_cast<const OctBf16*>(p)->w;
+  z[0] = bf16_lo(w.x); z[1] = bf16_hi(w.x); z[2] = bf16_lo(w.y); z[3] = bf16_hi(w.y);
+  z[4] = bf16_lo(w.z); z[5] = bf16_hi(w.z); z[6] = bf16_lo(w.w); z[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void load8(const float* p, float z[8]) {
+  const OctF32 v = *reinterpret_cast<const OctF32*>(p);
+  z[0] = __uint_as_float(v.a.x); z[1] = __uint_as_float(v.a.y);
+  z[2] = __uint_as_float(v.a.z); z[3] = __uint_as_float(v.a.w);
+  z[4] = __uint_as_float(v.b.x); z[5] = __uint_as_float(v.b.y);
+  z[6] = __uint_as_float(v.b.z); z[7] = __uint_as_float(v.b.w);
+}
+
+// Every element of a row by the whole workgroup: f(z cleaned, index).
+template <typename LT, int THREADS, typename F>
+__device__ __forceinline__ void each_logit(const LT* row, int V, F f) {
+  const int full = V / 8;
+  for (int o = threadIdx.x; o < full; o += THREADS) {
+    float z[8];
+    load8(row + o * 8, z);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f(clean_logit(z[j]), o * 8 + j);
+  }
+  const int e = full * 8 + threadIdx.x;
+  if (e < V) f(clean_logit(logit_at(row, e)), e);
+}
+
+}  // namespace sv

@@ -100,6 +100,80 @@ struct TreeLaunch {
   const float* temperatures = nullptr;
 };
 
+// Filter rows of B * per_seq logit rows (spec_draft_sample_filtered, and the
+// first kernel of spec_verify_filtered*).
+struct FilterLaunch {
+  const void* logits;            // rows of row_stride elements
+  long row_stride;
+  const int32_t* row_index;      // [B*per_seq] or NULL
+  long n_rows;
+  const float* uniforms;         // [B*per_seq], with out_tokens
+  const float* temperatures;     // [B] or NULL
+  float temperature;
+  const int32_t* top_ks;         // [B] or NULL, as the next two
+  const float* top_ps;
+  const float* min_ps;
+  int B, per_seq, V;
+  int bf16;
+  int32_t* out_tokens;           // may be NULL, as the next two
+  float* out_probs;
+  sv_filter_row* out_rows;
+  int32_t* device_error;         // may be NULL
+};
+
+struct FilteredVerifyLaunch {
+  const void* logits;            // [B][K+1] rows of row_stride elements
+  long row_stride;
+  const float* draft_probs;      // [B][K][V], or from the drafter's logits:
+  int lq;
+  const void* dlogits;           // rows of d_stride elements, same dtype
+  long d_stride, d_rows;
+  const int32_t* drows;          // [B*K] or NULL
+  const sv_filter_row* ddesc;    // [B*K]
+  const int32_t* draft_tokens;
+  const float* uniforms;
+  const float* temperatures;     // [B]
+  const int32_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+  int B, K, V;
+  int bf16;
+  int32_t* out_tokens;
+  int32_t* out_num_accepted;
+  float* out_p;                  // may be NULL
+  void* workspace;
+  int32_t* device_error;         // may be NULL
+  sv_filter_row* rows;           // [B*(K+1)], in the workspace (set by the launch)
+};
+
+struct AppendLaunch {
+  const void* query;             // NULL: no queries
+  const void* key;
+  const void* value;
+  int dtype;
+  long q_stride, k_stride, v_stride, out_q_stride;   // elements per row
+  const int64_t* positions;
+  const int64_t* slots;
+  const float* inv_freq;         // [rot / 2]
+  int rot, interleaved;
+  float rotary_scale;
+  long R;
+  int q_heads, kv_heads, head_dim;
+  void* key_cache;
+  void* value_cache;
+  int fp8;                       // caches hold e4m3 (else the source type)
+  long num_slots;
+  int block_size;
+  long block_stride, slot_stride, head_stride;       // cache elements
+  const float* k_scales;         // [kv_heads] or NULL (1), e4m3 only
+  const float* v_scales;
+  void* out_query;
+  int32_t* device_error;         // may be NULL
+  // set by launch_append
+  int items, rows_per_block;
+  unsigned row_magic, item_magic, vitem_magic;
+};
+
 // The row-statistics partials of a verify workspace: [B][K+1][S] entries.
 struct RowPartials {
   void* partials;
@@ -133,6 +207,11 @@ hipError_t launch_build(const BuildLaunch& L, hipStream_t stream);
 hipError_t launch_draft(const DraftLaunch& L, hipStream_t stream);
 hipError_t launch_metrics(const int32_t* num_accepted, int B, int K, uint64_t* metrics,
                           int32_t* device_error, hipStream_t stream);
+
+size_t filter_workspace_bytes(long n_rows, int V);
+hipError_t launch_filter_rows(const FilterLaunch& L, hipStream_t stream);
+hipError_t launch_filtered_verify(const FilteredVerifyLaunch& L, hipStream_t stream);
+hipError_t launch_append(const AppendLaunch& L, hipStream_t stream);
 
 // Pause kernel tracing on this host thread for the lifetime of the object
 // (graph capture records no timing events).

@@ -66,7 +66,9 @@ typedef enum {
 typedef enum {
   SV_F32 = 0,   /* IEEE binary32                                            */
   SV_BF16 = 1,  /* bfloat16 (upper half of a binary32)                      */
-  SV_F16 = 2    /* IEEE binary16: accepted where data is only copied (hidden) */
+  SV_F16 = 2,   /* IEEE binary16: hidden states, and queries, keys and values */
+  SV_E4M3 = 3   /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448,
+                   no infinities: key and value caches                       */
 } sv_dtype;
 
 /* Bits OR-ed into *device_error. */
@@ -86,6 +88,13 @@ typedef enum {
                                      infinite or too small for log2(e)/T to be a
                                      finite fp32 (T < ~4.24e-39): that sequence is
                                      treated as greedy (T = 0)                         */
+
+#define SV_DEVERR_FILTER 64       /* a per-sequence top-k below 0, top-p outside (0, 1] or min-p
+                                     outside [0, 1]: that filter is off for the sequence   */
+#define SV_DEVERR_EMPTY_ROW 128   /* a row without a logit above -inf in a filtered call: it
+                                     keeps no token; token 0 is drawn from it              */
+#define SV_DEVERR_SLOT 256        /* peagle_append_kv: a slot that is neither -1 nor in
+                                     [0, num_blocks * block_size): nothing is written      */
 
 /* Limits (a call outside them returns SV_ERR_SHAPE). */
 #define SV_MAX_B (1 << 20)        /* sequences per call                               */
@@ -586,6 +595,168 @@ SV_API sv_status spec_draft_sample(const void* drafter_logits, int logits_dtype,
                                    int32_t* device_error, void* stream);
 
 /*
+ * Filtered distributions.  The calls below restrict softmax(z / T) of a logit
+ * row z with the settings of its sequence, one filter after the other:
+ *   order     the tokens by logit, the largest first, equal logits by index;
+ *             -0 equals +0; -inf and NaN logits are never kept;
+ *   top-k     the first k tokens (0, or k >= V: off);
+ *   top-p     of those, a token is kept iff the probability of the tokens
+ *             before it, among those, is below p (1: off);
+ *   min-p     of those, a token is kept iff its probability is at least
+ *             min_p times the largest (0: off);
+ * and normalise what is kept.  The first token is always kept.  T = 0 keeps
+ * the first token alone (greedy).  Each filter keeps a prefix of the order, so
+ * 32 bytes describe the kept set of a row:
+ *   kept(x) iff z(x) > min_kept or (z(x) = min_kept and x <= last)
+ *   prob(x) = 2^((z(x) - max) scale) inv_sum  if kept(x), else 0    (in fp64)
+ * with z(x) = max giving 2^0 = 1 also where the maximum is +inf.
+ * Settings are per sequence, in device arrays of B entries: temperatures,
+ * top_ks (int32), top_ps and min_ps (fp32); a NULL array of the last three
+ * switches its filter off.  Bad values set SV_DEVERR_TEMPERATURE (the sequence
+ * is greedy) or SV_DEVERR_FILTER (the filter is off).
+ * Weights, their sums, every cut and every draw are evaluated in fp64, so that
+ * results agree with an exact evaluation unless a decision lies within ~1e-10
+ * of its threshold.
+ */
+typedef struct sv_filter_row {
+  double scale;      /* log2(e) / T; 0: greedy                                  */
+  double inv_sum;    /* 1 / sum over the kept tokens of 2^((z - max) scale)     */
+  float max;         /* the row's largest logit                                 */
+  float min_kept;    /* the logit of the last kept token in the order; -inf if
+                        no filter is on, +inf if nothing is kept               */
+  int32_t last;      /* the index of that token; V - 1 if no filter is on, -1 if
+                        nothing is kept                                         */
+  int32_t n_kept;    /* kept tokens; V if no filter is on                       */
+} sv_filter_row;
+
+/* Bytes of device workspace a filtered call needs for n_rows logit rows (B*K
+ * rows of the sampler, B*(K+1) of the verify).  Its contents do not matter and
+ * are not kept between calls.  Returns 0 for invalid sizes. */
+SV_API size_t spec_filter_workspace_bytes(int64_t n_rows, int V);
+
+/*
+ * Sampling from filtered distributions: spec_draft_sample with top-k, top-p
+ * and min-p.  With K = 1 and no row_index it is one decode step of B requests
+ * without drafts.  Source: as spec_draft_sample; the rskf.cn survey, section
+ * 2.1, names top-p and temperature sampling in the decode step.
+ *   drafter_logits   [n_rows] rows of V logits, row_stride elements apart
+ *                    (row_stride >= V: a padded vocabulary), SV_F32 or SV_BF16.
+ *   row_index, uniforms, temperature, temperatures, out_draft_tokens: as for
+ *                    spec_draft_sample.  The token is the smallest kept v
+ *                    whose running total of probabilities in vocabulary order
+ *                    exceeds uniforms[b][k] times their sum.
+ *   top_ks, top_ps, min_ps  optional [B], see above.
+ *   out_draft_probs  optional [B][K][V] fp32: the filtered, normalised q (0
+ *                    for tokens that are not kept).
+ *   out_filter_rows  optional [B][K] sv_filter_row, 16-byte aligned: what
+ *                    spec_verify_filtered_lq needs instead of a dense q.
+ *   workspace        spec_filter_workspace_bytes(B*K, V) bytes, 16-byte aligned.
+ * A row index outside [0, n_rows) sets SV_DEVERR_ROW_INDEX: token -1, q and
+ * filter row empty.  1 <= K <= SV_MAX_K, 1 <= V <= SV_MAX_V.
+ */
+SV_API sv_status spec_draft_sample_filtered(
+    const void* drafter_logits, int logits_dtype, int64_t n_rows, int64_t row_stride,
+    const int32_t* row_index, const float* uniforms, float temperature,
+    const float* temperatures, const int32_t* top_ks, const float* top_ps, const float* min_ps,
+    int B, int K, int V, int32_t* out_draft_tokens, float* out_draft_probs,
+    sv_filter_row* out_filter_rows, void* workspace, size_t workspace_bytes,
+    int32_t* device_error, void* stream);
+
+/*
+ * Sampled verify whose target distributions are filtered: rejection sampling
+ * as in spec_verify_mixed with p_k = the filtered distribution of row k, so
+ * that the emitted tokens follow exactly what sampling the target with those
+ * settings gives, whatever q the drafts were drawn from ("Project 14", section
+ * 架构; the rskf.cn survey, sections 1 and 2.2).
+ *   target_logits    [B][K+1] rows of V logits, row_stride elements apart.
+ *   draft_probs      [B][K][V] fp32, used as given.
+ *   draft_tokens, uniforms, temperatures, out_tokens, out_num_accepted,
+ *   out_draft_target_prob: as for spec_verify_mixed.  Draft k is accepted iff
+ *                    p_k(x) > 0 and u q_k(x) < p_k(x); sequences at T = 0
+ *                    accept iff the draft is the first token of the order.
+ *                    The new token is drawn from max(0, p_a - q_a), from p_a
+ *                    where that sums to 0 or a = K.
+ *   top_ks, top_ps, min_ps  optional [B], see above.
+ *   workspace        spec_filter_workspace_bytes(B*(K+1), V) bytes, 16-byte
+ *                    aligned.
+ * 0 <= K <= SV_MAX_K (K = 0: one token per sequence from its row).
+ */
+SV_API sv_status spec_verify_filtered(
+    const void* target_logits, int logits_dtype, int64_t row_stride, const float* draft_probs,
+    const int32_t* draft_tokens, const float* uniforms, const float* temperatures,
+    const int32_t* top_ks, const float* top_ps, const float* min_ps, int B, int K, int V,
+    int32_t* out_tokens, int32_t* out_num_accepted, float* out_draft_target_prob,
+    void* workspace, size_t workspace_bytes, int32_t* device_error, void* stream);
+
+/*
+ * spec_verify_filtered with q given as the drafter's logits and the filter
+ * rows of spec_draft_sample_filtered (as spec_verify_mixed_lq takes logits and
+ * sv_draft_row): q is evaluated in fp64 at the tokens the verify needs.
+ *   drafter_logits   [n_drafter_rows] rows of V logits, drafter_row_stride
+ *                    elements apart, same dtype as target_logits.
+ *   drafter_rows     optional [B][K] int32, as for spec_verify_sample_lq.
+ *   filter_rows      [B][K] sv_filter_row, 16-byte aligned.
+ */
+SV_API sv_status spec_verify_filtered_lq(
+    const void* target_logits, int logits_dtype, int64_t row_stride, const void* drafter_logits,
+    int64_t n_drafter_rows, int64_t drafter_row_stride, const int32_t* drafter_rows,
+    const sv_filter_row* filter_rows, const int32_t* draft_tokens, const float* uniforms,
+    const float* temperatures, const int32_t* top_ks, const float* top_ps, const float* min_ps,
+    int B, int K, int V, int32_t* out_tokens, int32_t* out_num_accepted,
+    float* out_draft_target_prob, void* workspace, size_t workspace_bytes,
+    int32_t* device_error, void* stream);
+
+/*
+ * Appends the keys and values of a batch of rows to a paged cache and applies
+ * the rotary position embedding to keys and queries on the way.  It reads what
+ * peagle_build_draft_batch writes: out_positions and out_slot_mapping, whose
+ * slot -1 (SV_PADDING_SLOT_ID) marks rejected rows that must not reach the
+ * cache (P-EAGLE / TorchSpec blog summary, section TorchSpec 集成与工程优化).
+ * For row r, head h and pair j < rotary_dim / 2, with the angle t =
+ * positions[r] * inv_freq[j] (in fp64, whatever the position):
+ *   (x0, x1) -> rotary_scale * (x0 cos t - x1 sin t, x1 cos t + x0 sin t),
+ * x0, x1 = elements j and j + rotary_dim/2 of the head, or 2j and 2j + 1 when
+ * interleaved != 0; elements from rotary_dim on are copied.  The products are
+ * fp32 and rounded once to the output's type.
+ *   query            optional [R][q_heads][head_dim], out_query likewise (the
+ *                    same buffer is allowed); rows without a slot are rotated
+ *                    too.  q_heads = 0 and NULL for none.
+ *   key, value       [R][kv_heads][head_dim], all of type dtype (SV_F32,
+ *                    SV_BF16 or SV_F16); rows are *_stride elements apart
+ *                    (views into one projection's output), heads dense.
+ *   positions, slot_mapping  [R] int64.  slot s is entry s % block_size of
+ *                    block s / block_size.  Rows that have a slot must have
+ *                    different ones; what a slot named twice holds afterwards
+ *                    is unspecified, element by element.
+ *   inv_freq         [rotary_dim / 2] fp32 (any frequency scaling is the
+ *                    caller's); may be NULL when rotary_dim = 0.
+ *   key_cache, value_cache  [num_blocks][block_size][kv_heads][head_dim] of
+ *                    type cache_dtype, entry (b, s, h, d) at b * block_stride
+ *                    + s * slot_stride + h * head_stride + d, so that caches
+ *                    with the heads outside the slots and halves of one
+ *                    key-and-value buffer are addressed in place.
+ *   cache_dtype      dtype, or SV_E4M3: round(x / scale[h]) limited to +-448
+ *                    (NaN stays NaN).
+ *   k_scales, v_scales  optional [kv_heads] fp32 (NULL: 1), SV_E4M3 only.
+ * Slots outside the cache set SV_DEVERR_SLOT and write nothing.  Cache entries
+ * that no row names are not touched.
+ * 1 <= head_dim <= SV_MAX_HEAD_DIM, rotary_dim even and in [0, head_dim],
+ * q_heads and kv_heads at most SV_MAX_HEADS, kv_heads >= 1, R < 2^31.  R = 0 is
+ * a no-op.  One kernel is enqueued.
+ */
+#define SV_MAX_HEAD_DIM 1024
+#define SV_MAX_HEADS 1024
+SV_API sv_status peagle_append_kv(
+    const void* query, const void* key, const void* value, int dtype, int64_t query_stride,
+    int64_t key_stride, int64_t value_stride, const int64_t* positions,
+    const int64_t* slot_mapping, const float* inv_freq, int rotary_dim, int interleaved,
+    float rotary_scale, int64_t R, int q_heads, int kv_heads, int head_dim, void* key_cache,
+    void* value_cache, int cache_dtype, int64_t num_blocks, int block_size,
+    int64_t block_stride, int64_t slot_stride, int64_t head_stride, const float* k_scales,
+    const float* v_scales, void* out_query, int64_t out_query_stride, int32_t* device_error,
+    void* stream);
+
+/*
  * Acceptance metrics, accumulated on the device.  `metrics` is an array of
  * spec_accept_metrics_words(K) uint64 counters in device memory, zeroed by the
  * caller once; every call adds one verify call's counts:
@@ -707,6 +878,9 @@ SV_API void sv_step_graph_destroy(sv_step_graph* graph);
 #define SV_KERNEL_ACCEPT_METRICS 8       /* spec_accept_metrics                          */
 #define SV_KERNEL_TREE_ROWS 9            /* spec_verify_tree: row statistics             */
 #define SV_KERNEL_TREE_WALK 10           /* spec_verify_tree: the walk down the tree     */
+#define SV_KERNEL_FILTER_ROWS 12         /* filtered calls: kept sets (sampler: and tokens)      */
+#define SV_KERNEL_FILTERED_VERIFY 13     /* spec_verify_filtered: accept scan and draw           */
+#define SV_KERNEL_APPEND_KV 14           /* peagle_append_kv                                     */
 
 SV_API const char* sv_kernel_name(int kernel_id);
 SV_API sv_status sv_trace_begin(int capacity, unsigned kernel_mask); /* SV_ERR_VALUE if capacity < 1 */

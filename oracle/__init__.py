@@ -41,6 +41,11 @@ of Eagle / MTP / DFlash / DSPark):
   law of the first emitted token on star trees (bisection over the uniforms,
   equal to the target softmax), chi-square on two-level trees, and a brute
   force check of the greedy walk.
+* ``filtered``                    rows restricted by top-k, top-p and min-p,
+  the verify on them, and the rotary embedding of the paged append.  Pinned by
+  brute force over every prefix of the order, hand-worked rows, the output law
+  of the verify (chi-square against the filtered target) and rotation by
+  complex numbers (tests/test_oracle_filtered.py).
 * ``peagle.build_draft_batch``    the P-EAGLE drafter batch.  Pinned by the
   invariants the P-EAGLE summary fixes (K-1 MASK rows per sequence, slot -1
   exactly on rejected tokens, h_shared on the MASK rows, the new token paired
@@ -49,7 +54,7 @@ of Eagle / MTP / DFlash / DSPark):
   the rejected padding rows are readings the pages leave open: those two
   aspects are parity unpinned by the pages.
 """
-from . import draft, metrics, mixed, peagle, tree, verify  # noqa: F401
+from . import draft, filtered, metrics, mixed, peagle, tree, verify  # noqa: F401
 from .mixed import verify_mixed  # noqa: F401
 from .draft import draft_distribution, draft_outcomes, draft_sample  # noqa: F401
 from .peagle import PADDING_SLOT_ID, build_draft_batch  # noqa: F401
