@@ -135,23 +135,46 @@ struct OpMin { template <typename T> __device__ T operator()(T a, T b) const { r
 // its element size, and gfx950 loads 16 bytes from any such address.
 struct __attribute__((packed, aligned(2))) OctBf16 { u32x4 w; };
 struct __attribute__((packed, aligned(4))) OctF32 { u32x4 a, b; };
-__device__ __forceinline__ void load8(const uint16_t* p, float z[8]) {
-  const u32x4 w = reinterpret_cast<const OctBf16*>(p)->w;
-  z[0] = bf16_lo(w.x); z[1] = bf16_hi(w.x); z[2] = bf16_lo(w.y); z[3] = bf16_hi(w.y);
-  z[4] = bf16_lo(w.z); z[5] = bf16_hi(w.z); z[6] = bf16_lo(w.w); z[7] = bf16_hi(w.w);
+__device__ __forceinline__ void raw8(const uint16_t* p, Raw<uint16_t>& r) {
+  r.w = reinterpret_cast<const OctBf16*>(p)->w;
 }
-__device__ __forceinline__ void load8(const float* p, float z[8]) {
+__device__ __forceinline__ void raw8(const float* p, Raw<float>& r) {
   const OctF32 v = *reinterpret_cast<const OctF32*>(p);
-  z[0] = __uint_as_float(v.a.x); z[1] = __uint_as_float(v.a.y);
-  z[2] = __uint_as_float(v.a.z); z[3] = __uint_as_float(v.a.w);
-  z[4] = __uint_as_float(v.b.x); z[5] = __uint_as_float(v.b.y);
-  z[6] = __uint_as_float(v.b.z); z[7] = __uint_as_float(v.b.w);
+  r.a = v.a;
+  r.b = v.b;
 }
+template <typename LT>
+__device__ __forceinline__ void load8(const LT* p, float z[8]) {
+  Raw<LT> r;
+  raw8(p, r);
+  unpack(r, z);
+}
+// Octets that reach past the row's end: the rest reads as -inf.
+__device__ __forceinline__ void raw8_end(const uint16_t* row, int e, int V, Raw<uint16_t>& r) {
+  uint32_t x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    x[j] = (e + 2 * j < V ? row[e + 2 * j] : 0xff80u) |
+           ((e + 2 * j + 1 < V ? row[e + 2 * j + 1] : 0xff80u) << 16);
+  r.w = u32x4{x[0], x[1], x[2], x[3]};
+}
+__device__ __forceinline__ void raw8_end(const float* row, int e, int V, Raw<float>& r) {
+  uint32_t x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = e + j < V ? __float_as_uint(row[e + j]) : 0xff800000u;
+  r.a = u32x4{x[0], x[1], x[2], x[3]};
+  r.b = u32x4{x[4], x[5], x[6], x[7]};
+}
+// An empty statement that claims to change a loaded octet, so that the
+// compiler unpacks it again instead of holding the unpacked values.
+__device__ __forceinline__ void keep_raw(Raw<uint16_t>& r) { asm volatile("" : "+v"(r.w)); }
+__device__ __forceinline__ void keep_raw(Raw<float>& r) { asm volatile("" : "+v"(r.a), "+v"(r.b)); }
 
 // Every element of a row by the whole workgroup: f(z cleaned, index).
 template <typename LT, int THREADS, typename F>
 __device__ __forceinline__ void each_logit(const LT* row, int V, F f) {
   const int full = V / 8;
+#pragma unroll 1
   for (int o = threadIdx.x; o < full; o += THREADS) {
     float z[8];
     load8(row + o * 8, z);

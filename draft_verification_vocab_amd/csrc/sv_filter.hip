@@ -9,6 +9,8 @@
 //   filtered_verify_kernel  one workgroup per sequence: the accept scan from
 //                        the filter rows, then the residual draw on the row
 //                        of the first rejection.
+#include <algorithm>
+
 #include "sv_filter.h"
 #include "sv_internal.h"
 
@@ -16,7 +18,6 @@ namespace sv {
 
 namespace {
 
-constexpr int kFilterThreads = 512;
 constexpr int kVerifyThreads = 256;
 constexpr int kBins = 2048;            // 11 key bits per level
 constexpr int kDrawTile = 2048;        // elements per tile of the draw
@@ -33,12 +34,13 @@ struct DrawShared {
 // whose running total exceeds u * sum, the last with any mass if rounding
 // leaves none, -1 if no token has mass.  Every thread gets it.
 template <int THREADS, typename F>
-__device__ int block_draw(int V, float u, DrawShared& sh, F mass) {
+__device__ __forceinline__ int block_draw(int V, float u, DrawShared& sh, F mass) {
   const int w = threadIdx.x / kWave, l = lane_id();
   const int tiles = (V + kDrawTile - 1) / kDrawTile;
   __syncthreads();
   for (int t = w; t < tiles; t += THREADS / kWave) {
     double s = 0.0;
+#pragma unroll 4
     for (int i = 0; i < kDrawTile / kWave; ++i) {
       const int e = t * kDrawTile + i * kWave + l;
       if (e < V) s += mass(e);
@@ -75,6 +77,7 @@ __device__ int block_draw(int V, float u, DrawShared& sh, F mass) {
       const int tile = __shfl(hits ? hit : any, src);
       double at = __shfl(before, src);
       int lastpos = -1;
+#pragma unroll 1
       for (int i = 0; i < kDrawTile / kWave && token < 0; ++i) {
         const int e = tile * kDrawTile + i * kWave + l;
         const double x = e < V ? mass(e) : 0.0;
@@ -116,7 +119,7 @@ __device__ __forceinline__ bool cut_keeps(const Cut& c, uint32_t key, int e) {
 
 // Index of the t-th token (t >= 1, in index order) whose key is `key`.
 template <typename LT, int THREADS>
-__device__ int nth_tie(const LT* row, int V, uint32_t key, int t, FilterShared<THREADS>& sh) {
+__device__ __forceinline__ int nth_tie(const LT* row, int V, uint32_t key, int t, FilterShared<THREADS>& sh) {
   const int tiles = (V + kDrawTile - 1) / kDrawTile;
   __syncthreads();
   for (int i = threadIdx.x; i < tiles; i += THREADS) sh.cnt[i] = 0;
@@ -134,6 +137,7 @@ __device__ int nth_tie(const LT* row, int V, uint32_t key, int t, FilterShared<T
       before += n;
     }
     int found = V - 1;
+#pragma unroll 1
     for (int i = 0; i < kDrawTile / kWave; ++i) {
       const int e = tile * kDrawTile + i * kWave + l;
       const bool is = e < V && logit_key(clean_logit(logit_at(row, e))) == key;
@@ -161,7 +165,7 @@ __device__ int nth_tie(const LT* row, int V, uint32_t key, int t, FilterShared<T
 // largest weight).  Only tokens that `in` keeps count.  Gives the key, the
 // number of its tokens (ties) and the total above it.
 template <typename LT, int THREADS, bool MASS>
-__device__ uint32_t radix_cut(const LT* row, int V, const Cut& in, float m, double c,
+__device__ __forceinline__ uint32_t radix_cut(const LT* row, int V, const Cut& in, float m, double c,
                               double target, int& ties, double& above, FilterShared<THREADS>& sh) {
   constexpr int PER = kBins / THREADS;
   static_assert(kBins % THREADS == 0, "whole bins per thread");
@@ -234,7 +238,7 @@ __device__ uint32_t radix_cut(const LT* row, int V, const Cut& in, float m, doub
 
 // The kept set of one row.  Workgroup-wide; every thread gets the filter row.
 template <typename LT, int THREADS>
-__device__ sv_filter_row filter_row(const LT* row, int V, const FilterSettings& s,
+__device__ __forceinline__ sv_filter_row filter_row(const LT* row, int V, const FilterSettings& s,
                                     FilterShared<THREADS>& sh) {
   float mx = -INFINITY;
   int nfin = 0;
@@ -321,13 +325,509 @@ __device__ sv_filter_row filter_row(const LT* row, int V, const FilterSettings& 
   return f;
 }
 
+// ---------------------------------------------------------------- one pass over a row
+// The logits are streamed once.  A wave takes tiles of 4096 elements, lane l
+// the octets u = 0..7 at 512 u + 8 l of a tile; every G octets of a lane are a
+// group, whose maximum goes to LDS (V / (8 G) of them).  The group maxima are
+// logits of the row, so the k-th largest of them is a lower bound of its k-th
+// largest logit: only groups whose maximum reaches a threshold found among
+// them (candidate groups) can hold kept tokens, and only those are read again.
+// Where a filter needs the row's whole sum (top-p without top-k, no filter at
+// all) the pass also leaves every tile's maximum and sum of weights.
+constexpr int kRowTile = 4096;
+constexpr int kRowTiles = SV_MAX_V / kRowTile;
+constexpr int kCand = 2048;            // candidate tokens a workgroup sorts in LDS
+constexpr int kQueue = 2048;           // candidate groups
+constexpr int kTopBins = 512;          // histogram of the group maxima
+constexpr int kMaxListK = 1024;        // largest top-k taken through the candidate list
+constexpr int kRankN = 256;            // most entries sorted by counting
+
+// Octets per group: 8, or fewer as long as there are at most 3200 groups.
+__host__ __device__ __forceinline__ int group_octets(int V) {
+  const int octs = (V + 7) / 8;
+  return octs <= 3200 ? 1 : octs <= 6400 ? 2 : octs <= 12800 ? 4 : 8;
+}
+
+template <int THREADS>
+struct RowShared {
+  unsigned long long list[kCand];      // candidates
+  union {
+    struct { uint32_t cnt[kTopBins], mass[kTopBins]; } top;
+    uint16_t queue[kQueue];
+    unsigned long long sorted[kRankN];
+  };
+  double tile_s[kRowTiles];
+  float tile_m[kRowTiles];
+  double red[THREADS / kWave];
+  int redi[THREADS / kWave];
+  int n, nq, token, bin, above;
+  float frac;
+};
+
+// n entries of sh.list in increasing order, in sh.list.  Workgroup-wide.
+template <int THREADS>
+__device__ __forceinline__ void sort_list(RowShared<THREADS>& sh, int n) {
+  __syncthreads();
+  if (n <= kRankN) {
+    // each entry's place is the number of smaller ones (no two are equal)
+    const int i = threadIdx.x;
+    unsigned long long x = 0;
+    int rank = 0;
+    if (i < n) {
+      x = sh.list[i];
+      for (int j = 0; j < n; ++j) rank += sh.list[j] < x;
+    }
+    __syncthreads();
+    if (i < n) sh.list[rank] = x;
+    __syncthreads();
+    return;
+  }
+  int N = 512;
+  while (N < n) N <<= 1;
+  for (int i = n + threadIdx.x; i < N; i += THREADS) sh.list[i] = ~0ull;
+  for (int size = 2; size <= N; size <<= 1)
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < N / 2; i += THREADS) {
+        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
+        const unsigned long long a = sh.list[lo], b = sh.list[hi];
+        if ((a > b) == ((lo & size) == 0)) { sh.list[lo] = b; sh.list[hi] = a; }
+      }
+    }
+  __syncthreads();
+}
+
+// Exclusive running totals over the workgroup's threads, and the total.
+template <int THREADS>
+__device__ __forceinline__ double block_scan(double x, double* sm, double& total) {
+  const double incl = wave_inclusive_scan(x);
+  __syncthreads();
+  if (lane_id() == kWave - 1) sm[threadIdx.x / kWave] = incl;
+  __syncthreads();
+  double off = 0.0, all = 0.0;
+#pragma unroll
+  for (int i = 0; i < THREADS / kWave; ++i) {
+    if (i < (int)threadIdx.x / kWave) off += sm[i];
+    all += sm[i];
+  }
+  total = all;
+  return off + (incl - x);
+}
+
+// Entries of the list: in the order, (~key, index); in vocabulary order,
+// (index, key).
+__device__ __forceinline__ unsigned long long order_entry(uint32_t key, int e) {
+  return ((unsigned long long)~key << 32) | (uint32_t)e;
+}
+
+template <typename LT, int THREADS, bool SUM>
+__device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G, float* gm,
+                           RowShared<THREADS>& sh, float& top, uint32_t& low) {
+  const int w = threadIdx.x / kWave, l = lane_id();
+  const int tiles = (V + kRowTile - 1) / kRowTile;
+  const int per = 8 / G;
+  for (int t = w; t < tiles; t += THREADS / kWave) {
+    Raw<LT> raw[8];
+    const int e0 = t * kRowTile + 8 * l;
+    if ((t + 1) * kRowTile <= V) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) raw8(row + e0 + u * kTile, raw[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int e = e0 + u * kTile;
+        if (e + 8 <= V) raw8(row + e, raw[u]);
+        else raw8_end(row, e, V, raw[u]);
+      }
+    }
+    float om[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      float z[8];
+      unpack(raw[u], z);
+      om[u] = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])),
+                    fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+    }
+    float mt = -INFINITY;
+    float g = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      g = fmaxf(g, om[u]);
+      if (((u + 1) & (G - 1)) == 0) {               // uniform
+        g = clean_logit(g);
+        gm[(t * per + u / G) * kWave + l] = g;
+        if (g > -INFINITY) low = min(low, logit_key(g));
+        mt = fmaxf(mt, g);
+        g = -INFINITY;
+      }
+    }
+    top = fmaxf(top, mt);
+    if constexpr (SUM) {
+      mt = wave_max(mt);
+      double s = 0.0, s1 = 0.0;
+      if (mt == INFINITY) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          keep_raw(raw[u]);
+          float z[8];
+          unpack(raw[u], z);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s += z[j] == INFINITY ? 1.0 : 0.0;
+        }
+      } else if (mt > -INFINITY) {
+        const double ref = -(double)mt * c;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          keep_raw(raw[u]);
+          float z[8];
+          unpack(raw[u], z);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            s += exp2_f64(fma((double)z[j], c, ref));
+            s1 += exp2_f64(fma((double)z[j + 1], c, ref));
+            __builtin_amdgcn_sched_barrier(0);      // two in flight: registers
+          }
+        }
+      }
+      s = wave_sum(s + s1);
+      if (l == 0) { sh.tile_m[t] = mt; sh.tile_s[t] = s; }
+    }
+  }
+}
+
+// The key from which on logits can be kept, from the group maxima: at least k
+// of them reach it (by count), or about `share` of the row's sum S lies in
+// logits that reach it (by mass).  Histograms of the maxima's keys, the first
+// over their whole range, then over the bin of the threshold while that bin is
+// wide.  A maximum stands for the group's tokens of its own size; in the
+// estimate of the mass, those hidden behind a larger one of their group are
+// added as 1 / (share of groups without a larger one).
+template <int THREADS>
+__device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, uint32_t kmax, uint32_t klow, float m,
+                                  float c, int k, float share_mass, RowShared<THREADS>& sh) {
+  const bool by_mass = k == 0;
+  uint32_t hi = kmax, lo = klow;       // the range of keys still searched
+  int above = 0;                       // groups above it
+  float mass = 0.f;                    // estimated mass above it, in units of the maximum
+#pragma unroll 1
+  for (int level = 0; level < 4; ++level) {
+    int shift = 0;
+    while (((hi - lo) >> shift) >= (uint32_t)kTopBins) ++shift;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTopBins; i += THREADS) sh.top.cnt[i] = sh.top.mass[i] = 0;
+    if (threadIdx.x == 0) sh.bin = -1;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < groups; i += THREADS) {
+      const float g = gm[i];
+      const uint32_t key = logit_key(g);
+      if (key <= hi && key >= lo) {
+        const uint32_t b = (hi - key) >> shift;
+        atomicAdd(&sh.top.cnt[b], 1u);
+        if (by_mass)
+          atomicAdd(&sh.top.mass[b],
+                    g == m ? 262144u : (uint32_t)(__builtin_amdgcn_exp2f((g - m) * c) * 262144.f));
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+      constexpr int PER = kTopBins / kWave;
+      const int l = lane_id();
+      int n[PER], mine = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) { n[i] = sh.top.cnt[l * PER + i]; mine += n[i]; }
+      int run = mine;
+#pragma unroll
+      for (int off = 1; off < kWave; off <<= 1) {
+        const int y = __shfl_up(run, off);
+        if (l >= off) run += y;
+      }
+      run += above - mine;
+      int hit = -1, before = 0;
+      float fbefore = 0.f;
+      if (!by_mass) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if (hit < 0 && run < k && run + n[i] >= k) { hit = l * PER + i; before = run; }
+          run += n[i];
+        }
+      } else {
+        float f[PER], fmine = 0.f;
+        int r = run;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          f[i] = (float)sh.top.mass[l * PER + i] * (1.f / 262144.f) *
+                 ((float)groups * __builtin_amdgcn_rcpf((float)max(1, groups - r)));
+          r += n[i];
+          fmine += f[i];
+        }
+        float frun = fmine;
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) {
+          const float y = __shfl_up(frun, off);
+          if (l >= off) frun += y;
+        }
+        frun += mass - fmine;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if (hit < 0 && n[i] && frun + f[i] >= share_mass) {
+            hit = l * PER + i; before = run; fbefore = frun;
+          }
+          run += n[i];
+          frun += f[i];
+        }
+      }
+      const unsigned long long hits = __ballot(hit >= 0);
+      if (hits && l == __ffsll((long long)hits) - 1) {
+        sh.bin = hit; sh.above = before; sh.frac = fbefore;
+      }
+    }
+    __syncthreads();
+    const int b = sh.bin;
+    if (b < 0) return kKeyNegInf + 1;               // not reached: every token
+    above = sh.above;
+    mass = sh.frac;
+    const int in = (int)sh.top.cnt[b];
+    const uint32_t top = hi - ((uint32_t)b << shift);
+    const uint32_t width = (1u << shift) - 1;
+    const uint32_t bottom = top - lo > width ? top - width : lo;
+    if (in <= above / 4 + 32 || shift == 0) return bottom;
+    hi = top;
+    lo = bottom;
+  }
+  return lo;
+}
+
+// The kept set of one row through the candidate list.  Returns false where the
+// row has to take the general path (filter_row): more candidates than the list
+// holds, or a large top-k.  `order` asks for the kept
+// tokens in vocabulary order: entries (index, key) in sh.list[0 .. count).
+template <typename LT, int THREADS>
+__device__ __forceinline__ bool filter_row_list(const LT* row, int V, const FilterSettings& s, bool order, float* gm,
+                                RowShared<THREADS>& sh, sv_filter_row& f, int& count) {
+  const int G = group_octets(V), per = 8 / G;
+  const int tiles = (V + kRowTile - 1) / kRowTile;
+  const int groups = tiles * per * kWave;
+  const bool by_k = s.k < V;
+  const bool all = V <= kCand;                      // every token fits the list
+  const bool need_sum = !all && !by_k && (s.p < 1.0 || s.off);
+  count = -1;
+  if (by_k && !all && s.k > kMaxListK) return false;
+  float top = -INFINITY;
+  uint32_t low = 0xffffffffu;
+  if (need_sum) stream_row<LT, THREADS, true>(row, V, s.c, G, gm, sh, top, low);
+  else stream_row<LT, THREADS, false>(row, V, s.c, G, gm, sh, top, low);
+  const float m = block_reduce<THREADS>(top, reinterpret_cast<float*>(sh.redi), OpMax());
+  low = block_reduce<THREADS>(low, reinterpret_cast<uint32_t*>(sh.redi), OpMin());
+  f = sv_filter_row{s.c, 0.0, m, INFINITY, -1, 0};
+  if (m == -INFINITY) { count = 0; return true; }
+  double S = 0.0;
+  if (need_sum) {
+    double part = 0.0;
+#pragma unroll 1
+    for (int t = threadIdx.x; t < tiles; t += THREADS) {
+      const double x = sh.tile_m[t] > -INFINITY
+                           ? sh.tile_s[t] * weight(sh.tile_m[t], m, s.c) : 0.0;
+      sh.tile_s[t] = x;
+      part += x;
+    }
+    S = block_reduce<THREADS>(part, sh.red, OpAdd());
+    if (s.off) {
+      f.inv_sum = 1.0 / S;
+      f.min_kept = -INFINITY;
+      f.last = V - 1;
+      f.n_kept = V;
+      return true;
+    }
+  }
+
+  // the lowest key a kept token can have
+  const uint32_t kmax = logit_key(m);
+  uint32_t mp_key = kKeyNegInf + 1;
+  if (s.mp > 0.0 && s.c > 0.0) {
+    // z >= m + log2(min_p) / c, a little lower: the exact test follows
+    const float z = (float)((double)m + ((double)__builtin_amdgcn_logf((float)s.mp) - 1e-4) / s.c);
+    mp_key = max(mp_key, min(kmax, logit_key(clean_logit(z)) - 2));
+  }
+  bool complete = true;                             // the list holds every kept token
+  for (int attempt = 0;; ++attempt) {
+    uint32_t kt = kKeyNegInf + 1;
+    if (!all) {
+      if (by_k) {
+        kt = s.k == 1 ? kmax : threshold_key<THREADS>(gm, groups, kmax, low, m, 0.f, s.k, 0.f, sh);
+        if (s.p >= 1.0) kt = max(kt, mp_key);
+      } else if (s.p < 1.0) {
+        // aim a little past the share p of the sum, further if that fell short
+        const double aim = s.p + (1.0 - s.p) * (attempt == 0 ? 0.25 : 0.75);
+        kt = threshold_key<THREADS>(gm, groups, kmax, low, m, (float)s.c, 0, (float)(aim * S), sh);
+        complete = kt <= mp_key;
+        kt = max(kt, mp_key);
+      } else {
+        kt = mp_key;
+      }
+    }
+    // candidate groups, then their tokens
+    __syncthreads();
+    if (threadIdx.x == 0) { sh.nq = 0; sh.n = 0; }
+    __syncthreads();
+    const float zt = key_logit(kt);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < groups; i += THREADS)
+      if (gm[i] >= zt) {
+        const int q = atomicAdd(&sh.nq, 1);
+        if (q < kQueue) sh.queue[q] = (uint16_t)i;
+      }
+    __syncthreads();
+    const int nq = sh.nq;
+    if (nq > kQueue) return false;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < nq * G; i += THREADS) {
+      const int q = sh.queue[i / G], u = q / kWave % per * G + i % G;
+      const int e = q / (per * kWave) * kRowTile + u * kTile + q % kWave * 8;
+      float z[8];
+      if (e + 8 <= V) {
+        load8(row + e, z);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = e + j < V ? logit_at(row, e + j) : -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = clean_logit(z[j]);
+        if (x >= zt) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kCand) sh.list[at] = order_entry(logit_key(x), e + j);
+        }
+      }
+    }
+    __syncthreads();
+    const int n = sh.n;
+    if (n > kCand) return false;
+    sort_list<THREADS>(sh, n);
+
+    // top-k, top-p and min-p along the order
+    const int nk = by_k ? min(n, s.k) : n;
+    const int chunk = (nk + THREADS - 1) / THREADS;
+    const int r0 = min((int)threadIdx.x * chunk, nk), r1 = min(r0 + chunk, nk);
+    const auto weight_of = [&](int r) {
+      return weight(key_logit(~(uint32_t)(sh.list[r] >> 32)), m, s.c);
+    };
+    double part = 0.0, total;
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) part += weight_of(r);
+    double run = block_scan<THREADS>(part, sh.red, total);
+    const double target = s.p * (need_sum ? S : total);
+    if (!complete && total < target) {
+      if (attempt) return false;
+      continue;
+    }
+    int keep = 0;
+    part = 0.0;
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+      const double w = weight_of(r);
+      if ((s.p >= 1.0 || run < target) && w >= s.mp) { ++keep; part += w; }
+      run += w;
+    }
+    keep = block_reduce<THREADS>(keep, sh.redi, OpAdd());
+    f.inv_sum = 1.0 / block_reduce<THREADS>(part, sh.red, OpAdd());
+    const unsigned long long last = sh.list[keep - 1];
+    f.min_kept = s.off ? -INFINITY : key_logit(~(uint32_t)(last >> 32));
+    f.last = s.off ? V - 1 : (int)(uint32_t)last;
+    f.n_kept = s.off ? V : keep;
+    count = keep;
+    if (order) {
+      __syncthreads();
+      for (int r = threadIdx.x; r < keep; r += THREADS) {
+        const unsigned long long x = sh.list[r];
+        sh.list[r] = (x << 32) | (uint32_t)~(x >> 32);
+      }
+      sort_list<THREADS>(sh, keep);
+    }
+    return true;
+  }
+}
+
+// The token drawn with uniform u from `count` entries in vocabulary order.
+template <int THREADS>
+__device__ __forceinline__ int draw_list(RowShared<THREADS>& sh, int count, float u, float m, double c) {
+  const int chunk = (count + THREADS - 1) / THREADS;
+  const int r0 = min((int)threadIdx.x * chunk, count), r1 = min(r0 + chunk, count);
+  double part = 0.0, total;
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) part += weight(key_logit((uint32_t)sh.list[r]), m, c);
+  double run = block_scan<THREADS>(part, sh.red, total);
+  const double target = (double)u * total;
+  int first = INT32_MAX, any = -1;
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    const double w = weight(key_logit((uint32_t)sh.list[r]), m, c);
+    run += w;
+    if (w > 0.0) {
+      any = r;
+      if (run > target) first = min(first, r);
+    }
+  }
+  first = block_reduce<THREADS>(first, sh.redi, OpMin());
+  any = block_reduce<THREADS>(any, sh.redi, OpMax());
+  return (int)(sh.list[first == INT32_MAX ? any : first] >> 32);
+}
+
+// The token drawn from a row without filters, whose tile masses stream_row
+// left in sh.tile_s.
+template <typename LT, int THREADS>
+__device__ __forceinline__ int draw_tiles(const LT* row, int V, RowShared<THREADS>& sh, float u, float m, double c) {
+  const int l = lane_id();
+  const int tiles = (V + kRowTile - 1) / kRowTile;
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    constexpr int PER = kRowTiles / kWave;
+    double x[PER], mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      x[i] = l * PER + i < tiles ? sh.tile_s[l * PER + i] : 0.0;
+      mine += x[i];
+    }
+    const double incl = wave_inclusive_scan(mine);
+    const double target = (double)u * __shfl(incl, kWave - 1);
+    double run = incl - mine, before = 0.0;
+    int hit = -1, any = -1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (x[i] > 0.0) {
+        any = l * PER + i;
+        if (hit < 0 && run + x[i] > target) { hit = l * PER + i; before = run; }
+      }
+      run += x[i];
+    }
+    const unsigned long long hits = __ballot(hit >= 0), anys = __ballot(any >= 0);
+    const int src = hits ? __ffsll((long long)hits) - 1 : 63 - __clzll((long long)anys);
+    const int tile = __shfl(hits ? hit : any, src);
+    double at = __shfl(before, src);
+    int token = -1, lastpos = 0;
+#pragma unroll 1
+    for (int i = 0; i < kRowTile / kWave && token < 0; ++i) {
+      const int e0 = tile * kRowTile + i * kWave, e = e0 + l;
+      const double y = e < V ? weight(clean_logit(logit_at(row, e)), m, c) : 0.0;
+      const double in = wave_inclusive_scan(y);
+      const unsigned long long pos = __ballot(y > 0.0);
+      if (pos) lastpos = e0 + 63 - __clzll((long long)pos);
+      const unsigned long long over = __ballot(y > 0.0 && at + in > target);
+      if (hits && over) token = e0 + __ffsll((long long)over) - 1;
+      at += __shfl(in, kWave - 1);
+    }
+    if (l == 0) sh.token = token < 0 ? lastpos : token;
+  }
+  __syncthreads();
+  return sh.token;
+}
+
 // ---------------------------------------------------------------- kernels
-template <typename LT>
-__global__ __launch_bounds__(kFilterThreads) void filter_rows_kernel(FilterLaunch A) {
-  __shared__ union {
-    FilterShared<kFilterThreads> filter;
-    DrawShared draw;
-  } sh;
+template <typename LT, int THREADS>
+__global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  RowShared<THREADS>& sh = *reinterpret_cast<RowShared<THREADS>*>(lds);
+  float* gm = reinterpret_cast<float*>(lds + sizeof(RowShared<THREADS>));
   const long r = blockIdx.x;
   const int b = (int)(r / A.per_seq);
   const int V = A.V;
@@ -338,34 +838,62 @@ __global__ __launch_bounds__(kFilterThreads) void filter_rows_kernel(FilterLaunc
   const bool there = ri >= 0 && ri < A.n_rows;
   sv_filter_row f{0.0, 0.0, -INFINITY, INFINITY, -1, 0};
   const LT* row = static_cast<const LT*>(A.logits) + (there ? ri : 0) * A.row_stride;
-  if (there) f = filter_row<LT, kFilterThreads>(row, V, s, sh.filter);
+  int count = 0;                                    // entries in sh.list; -1: none, not a list
+  bool general = false;
+  if (there) {
+    general = !filter_row_list<LT, THREADS>(row, V, s, A.out_tokens || A.lists, gm, sh, f, count);
+    if (general) {
+      __syncthreads();
+      f = filter_row<LT, THREADS>(row, V, s, *reinterpret_cast<FilterShared<THREADS>*>(lds));
+      count = -1;
+    }
+  }
   if (!there) errors |= SV_DEVERR_ROW_INDEX;
   else if (f.n_kept == 0) errors |= SV_DEVERR_EMPTY_ROW;
   if (threadIdx.x == 0) {
     if (errors) flag_error(A.device_error, errors);
     if (A.out_rows) A.out_rows[r] = f;
+    if (A.lists) A.list_counts[r] = count;
   }
+  if (A.lists)
+    for (int i = threadIdx.x; i < count; i += THREADS)
+      A.lists[r * kCand + i] = (int32_t)(sh.list[i] >> 32);
   if (A.out_tokens) {
     int token = there ? 0 : -1;
     if (f.n_kept > 0) {
-      token = s.c == 0.0 ? f.last
-                         : block_draw<kFilterThreads>(V, A.uniforms[r], sh.draw, [&](int e) {
-                             const float z = clean_logit(logit_at(row, e));
-                             return row_keeps(f, z, e) ? weight(z, f.max, f.scale) : 0.0;
-                           });
+      if (s.c == 0.0) token = f.last;
+      else if (count > 0) token = draw_list<THREADS>(sh, count, A.uniforms[r], f.max, s.c);
+      else if (!general) token = draw_tiles<LT, THREADS>(row, V, sh, A.uniforms[r], f.max, s.c);
+      else
+        token = block_draw<THREADS>(V, A.uniforms[r], *reinterpret_cast<DrawShared*>(lds),
+                                    [&](int e) {
+                                      const float z = clean_logit(logit_at(row, e));
+                                      return row_keeps(f, z, e) ? weight(z, f.max, f.scale) : 0.0;
+                                    });
     }
     if (threadIdx.x == 0) A.out_tokens[r] = token;
   }
   if (A.out_probs) {
     float* q = A.out_probs + r * V;
-    for (int e = threadIdx.x; e < V; e += kFilterThreads)
-      __builtin_nontemporal_store(f.n_kept ? (float)row_prob(f, logit_at(row, e), e) : 0.f, q + e);
+    if (count >= 0) {
+      for (int e = threadIdx.x; e < V; e += THREADS) __builtin_nontemporal_store(0.f, q + e);
+      __syncthreads();                              // the kept tokens' own values after the zeros
+      for (int i = threadIdx.x; i < count; i += THREADS) {
+        const unsigned long long x = sh.list[i];
+        q[x >> 32] = (float)(weight(key_logit((uint32_t)x), f.max, f.scale) * f.inv_sum);
+      }
+    } else {
+      for (int e = threadIdx.x; e < V; e += THREADS)
+        __builtin_nontemporal_store((float)row_prob(f, logit_at(row, e), e), q + e);
+    }
   }
 }
 
 template <typename LT, bool QL>
 __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(FilteredVerifyLaunch A) {
   __shared__ DrawShared draw;
+  __shared__ double red[kVerifyThreads / kWave];
+  __shared__ int redi[kVerifyThreads / kWave];
   __shared__ int sh_a;
   const int b = blockIdx.x, K = A.K, V = A.V;
   const int l = lane_id();
@@ -428,8 +956,48 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
     token = f.last;
   } else {
     const float u = A.uniforms[row0 + K];
+    const int count = A.list_counts[row0 + a];
     token = -1;
-    if (a < K) {
+    if (count >= 0) {
+      // the kept tokens alone, in vocabulary order
+      const int32_t* list = A.lists + (row0 + a) * kCand;
+      const long dr = a < K ? drafter_row(a) : -1;
+      sv_filter_row fq{};
+      if constexpr (QL) { if (a < K) fq = A.ddesc[(long)b * K + a]; }
+      const int chunk = (count + kVerifyThreads - 1) / kVerifyThreads;
+      const int r0 = min((int)threadIdx.x * chunk, count), r1 = min(r0 + chunk, count);
+      double r[kCand / kVerifyThreads], p[kCand / kVerifyThreads], rs = 0.0, ps = 0.0, total;
+#pragma unroll
+      for (int i = 0; i < kCand / kVerifyThreads; ++i) {
+        r[i] = p[i] = 0.0;
+        if (r0 + i < r1) {
+          const int e = list[r0 + i];
+          p[i] = row_prob(f, logit_at(za, e), e);
+          r[i] = a < K ? fmax(0.0, p[i] - q_at(a, dr, fq, e)) : p[i];
+        }
+        rs += r[i];
+        ps += p[i];
+      }
+      double run = block_scan<kVerifyThreads>(rs, red, total);
+      if (!(total > 0.0)) {                          // q covers p: draw from p
+        run = block_scan<kVerifyThreads>(ps, red, total);
+#pragma unroll
+        for (int i = 0; i < kCand / kVerifyThreads; ++i) r[i] = p[i];
+      }
+      const double target = (double)u * total;
+      int first = INT32_MAX, any = -1;
+#pragma unroll
+      for (int i = 0; i < kCand / kVerifyThreads; ++i) {
+        run += r[i];
+        if (r[i] > 0.0) {
+          any = r0 + i;
+          if (run > target) first = min(first, r0 + i);
+        }
+      }
+      first = block_reduce<kVerifyThreads>(first, redi, OpMin());
+      any = block_reduce<kVerifyThreads>(any, redi, OpMax());
+      token = list[first == INT32_MAX ? any : first];
+    } else if (a < K) {
       const long dr = drafter_row(a);
       sv_filter_row fq{};
       if constexpr (QL) fq = A.ddesc[(long)b * K + a];
@@ -449,21 +1017,42 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
 
 size_t filter_workspace_bytes(long n_rows, int V) {
   (void)V;
-  return (size_t)n_rows * sizeof(sv_filter_row);
+  return (size_t)n_rows * (sizeof(sv_filter_row) + (kCand + 4) * sizeof(int32_t));
 }
 
+namespace {
+template <typename LT, int THREADS>
+void launch_rows(const FilterLaunch& L, hipStream_t stream) {
+  const int tiles = (L.V + kRowTile - 1) / kRowTile;
+  const size_t gm = (size_t)tiles * (8 / group_octets(L.V)) * kWave * sizeof(float);
+  const size_t lds = std::max(sizeof(RowShared<THREADS>) + gm, sizeof(FilterShared<THREADS>));
+  filter_rows_kernel<LT, THREADS>
+      <<<dim3((unsigned)((long)L.B * L.per_seq)), THREADS, lds, stream>>>(L);
+}
+}  // namespace
+
 hipError_t launch_filter_rows(const FilterLaunch& L, hipStream_t stream) {
-  const dim3 grid((unsigned)((long)L.B * L.per_seq));
+  // one workgroup per row: a large one while rows leave CUs idle
+  const bool few = (long)L.B * L.per_seq <= 512;
   trace_before(stream, SV_KERNEL_FILTER_ROWS);
-  if (L.bf16) filter_rows_kernel<uint16_t><<<grid, kFilterThreads, 0, stream>>>(L);
-  else filter_rows_kernel<float><<<grid, kFilterThreads, 0, stream>>>(L);
+  if (L.bf16) {
+    if (few) launch_rows<uint16_t, 1024>(L, stream);
+    else launch_rows<uint16_t, 256>(L, stream);
+  } else {
+    if (few) launch_rows<float, 1024>(L, stream);
+    else launch_rows<float, 256>(L, stream);
+  }
   trace_after(stream, SV_KERNEL_FILTER_ROWS);
   return hipGetLastError();
 }
 
 hipError_t launch_filtered_verify(const FilteredVerifyLaunch& L0, hipStream_t stream) {
   FilteredVerifyLaunch L = L0;
+  // workspace: filter rows, kept-token counts, kept tokens
+  const long rows = (long)L.B * (L.K + 1);
   L.rows = static_cast<sv_filter_row*>(L.workspace);
+  L.list_counts = reinterpret_cast<int32_t*>(L.rows + rows);
+  L.lists = L.list_counts + (rows + 3) / 4 * 4;
   FilterLaunch F{};
   F.logits = L.logits;
   F.row_stride = L.row_stride;
@@ -478,6 +1067,8 @@ hipError_t launch_filtered_verify(const FilteredVerifyLaunch& L0, hipStream_t st
   F.V = L.V;
   F.bf16 = L.bf16;
   F.out_rows = L.rows;
+  F.lists = L.lists;
+  F.list_counts = L.list_counts;
   F.device_error = L.device_error;
   hipError_t e = launch_filter_rows(F, stream);
   if (e != hipSuccess) return e;

@@ -118,6 +118,8 @@ struct FilterLaunch {
   int32_t* out_tokens;           // may be NULL, as the next two
   float* out_probs;
   sv_filter_row* out_rows;
+  int32_t* lists;                // kept tokens in vocabulary order, for the verify, or NULL
+  int32_t* list_counts;          // their number per row; -1: no list
   int32_t* device_error;         // may be NULL
 };
 
@@ -143,7 +145,10 @@ struct FilteredVerifyLaunch {
   float* out_p;                  // may be NULL
   void* workspace;
   int32_t* device_error;         // may be NULL
-  sv_filter_row* rows;           // [B*(K+1)], in the workspace (set by the launch)
+  // in the workspace, set by the launch
+  sv_filter_row* rows;           // [B*(K+1)]
+  int32_t* list_counts;
+  int32_t* lists;
 };
 
 struct AppendLaunch {
