@@ -716,6 +716,7 @@ SV_API sv_status spec_draft_sample_filtered(
   L.out_tokens = out_draft_tokens;
   L.out_probs = out_draft_probs;
   L.out_rows = out_filter_rows;
+  L.workspace = workspace;
   L.device_error = device_error;
   return sv::launch_filter_rows(L, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK
                                                                                    : SV_ERR_HIP;

@@ -358,6 +358,7 @@ struct RowShared {
   };
   double tile_s[kRowTiles];
   float tile_m[kRowTiles];
+  double table[kExpTable];
   double red[THREADS / kWave];
   int redi[THREADS / kWave];
   int n, nq, token, bin, above;
@@ -420,13 +421,16 @@ __device__ __forceinline__ unsigned long long order_entry(uint32_t key, int e) {
   return ((unsigned long long)~key << 32) | (uint32_t)e;
 }
 
-template <typename LT, int THREADS, bool SUM>
-__device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G, float* gm,
-                           RowShared<THREADS>& sh, float& top, uint32_t& low) {
-  const int w = threadIdx.x / kWave, l = lane_id();
-  const int tiles = (V + kRowTile - 1) / kRowTile;
+// One wave's tile t of a row: its groups' maxima to gm (the row's), with SUM
+// its maximum and sum of weights to *tile_m, *tile_s.  Gives the lane's largest
+// logit and its groups' lowest key above -inf.
+template <typename LT, bool SUM>
+__device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double c, int G, float* gm,
+                                            float* tile_m, double* tile_s, const double* table,
+                                            float& top, uint32_t& low) {
+  const int l = lane_id();
   const int per = 8 / G;
-  for (int t = w; t < tiles; t += THREADS / kWave) {
+  {
     Raw<LT> raw[8];
     const int e0 = t * kRowTile + 8 * l;
     if ((t + 1) * kRowTile <= V) {
@@ -465,16 +469,12 @@ __device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G
     if constexpr (SUM) {
       mt = wave_max(mt);
       double s = 0.0, s1 = 0.0;
-      if (mt == INFINITY) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          keep_raw(raw[u]);
-          float z[8];
-          unpack(raw[u], z);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s += z[j] == INFINITY ? 1.0 : 0.0;
-        }
-      } else if (mt > -INFINITY) {
+      // Logits 500 octaves and more below the maximum (and -inf, NaN) count
+      // 2^-500.  Where z c loses too much in fp64, or that floor cannot be told
+      // from the maximum in fp32 (huge or infinite logits, huge temperatures),
+      // each weight is computed by itself.
+      const float floor = (float)((double)mt - 500.0 / c);
+      if (fabs((double)mt) * c < 4096.0 && floor < mt && floor > -INFINITY) {
         const double ref = -(double)mt * c;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -483,16 +483,54 @@ __device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G
           unpack(raw[u], z);
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            s += exp2_f64(fma((double)z[j], c, ref));
-            s1 += exp2_f64(fma((double)z[j + 1], c, ref));
-            __builtin_amdgcn_sched_barrier(0);      // two in flight: registers
+            s += exp2_table(fma((double)fmaxf(z[j], floor), c, ref), table);
+            s1 += exp2_table(fma((double)fmaxf(z[j + 1], floor), c, ref), table);
           }
+          __builtin_amdgcn_sched_barrier(0);        // one octet in flight: registers
+        }
+      } else if (mt > -INFINITY) {
+#pragma unroll 1
+        for (int i = 0; i < kRowTile / kWave; ++i) {
+          const int e = t * kRowTile + i * kWave + l;
+          if (e < V) s += weight(clean_logit(logit_at(row, e)), mt, c);
         }
       }
       s = wave_sum(s + s1);
-      if (l == 0) { sh.tile_m[t] = mt; sh.tile_s[t] = s; }
+      if (l == 0) { *tile_m = mt; *tile_s = s; }
     }
   }
+}
+
+// A whole row by one workgroup, into LDS.
+template <typename LT, int THREADS, bool SUM>
+__device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G, float* gm,
+                                           RowShared<THREADS>& sh, float& top, uint32_t& low) {
+  const int tiles = (V + kRowTile - 1) / kRowTile;
+  if constexpr (SUM) {
+    fill_exp_table(sh.table, threadIdx.x, THREADS);
+    __syncthreads();
+  }
+  for (int t = threadIdx.x / kWave; t < tiles; t += THREADS / kWave)
+    stream_tile<LT, SUM>(row, V, t, c, G, gm, &sh.tile_m[t], &sh.tile_s[t], sh.table, top, low);
+}
+
+// What a row's stream leaves, where a kernel of its own made it: into LDS.
+template <int THREADS>
+__device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int groups, int tiles,
+                                              bool sum, float* gm, RowShared<THREADS>& sh,
+                                              float& top, uint32_t& low) {
+  const float* g = A.group_max + r * groups;
+  for (int i = threadIdx.x; i < groups; i += THREADS) {
+    const float x = g[i];
+    gm[i] = x;
+    top = fmaxf(top, x);
+    if (x > -INFINITY) low = min(low, logit_key(x));
+  }
+  if (sum)
+    for (int t = threadIdx.x; t < tiles; t += THREADS) {
+      sh.tile_m[t] = A.tile_max[r * tiles + t];
+      sh.tile_s[t] = A.tile_sum[r * tiles + t];
+    }
 }
 
 // The key from which on logits can be kept, from the group maxima: at least k
@@ -501,14 +539,15 @@ __device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G
 // over their whole range, then over the bin of the threshold while that bin is
 // wide.  A maximum stands for the group's tokens of its own size; in the
 // estimate of the mass, those hidden behind a larger one of their group are
-// added as 1 / (share of groups without a larger one).
+// added as 1 / (share of groups without a larger one).  The search starts at
+// key `hi`, `above` groups lying above it.
 template <int THREADS>
-__device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, uint32_t kmax, uint32_t klow, float m,
-                                  float c, int k, float share_mass, RowShared<THREADS>& sh) {
+__device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, uint32_t hi,
+                                                  uint32_t lo, int above, float m, float c, int k,
+                                                  float share_mass, RowShared<THREADS>& sh) {
   const bool by_mass = k == 0;
-  uint32_t hi = kmax, lo = klow;       // the range of keys still searched
-  int above = 0;                       // groups above it
-  float mass = 0.f;                    // estimated mass above it, in units of the maximum
+  if (hi < lo) return kKeyNegInf + 1;
+  float mass = 0.f;                    // estimated mass found, in units of the maximum
 #pragma unroll 1
   for (int level = 0; level < 4; ++level) {
     int shift = 0;
@@ -598,24 +637,31 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
   return lo;
 }
 
+// Whether a row's filters need the sum of all its weights: no top-k bounds the
+// tokens that matter, and they do not all fit the candidate list.
+__device__ __forceinline__ bool row_needs_sum(const FilterSettings& s, int V) {
+  return V > kCand && s.k >= V && (s.p < 1.0 || s.off);
+}
+
 // The kept set of one row through the candidate list.  Returns false where the
 // row has to take the general path (filter_row): more candidates than the list
 // holds, or a large top-k.  `order` asks for the kept
 // tokens in vocabulary order: entries (index, key) in sh.list[0 .. count).
-template <typename LT, int THREADS>
-__device__ __forceinline__ bool filter_row_list(const LT* row, int V, const FilterSettings& s, bool order, float* gm,
+template <typename LT, int THREADS, bool PRE>
+__device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, const LT* row, int V, const FilterSettings& s, bool order, float* gm,
                                 RowShared<THREADS>& sh, sv_filter_row& f, int& count) {
   const int G = group_octets(V), per = 8 / G;
   const int tiles = (V + kRowTile - 1) / kRowTile;
   const int groups = tiles * per * kWave;
   const bool by_k = s.k < V;
   const bool all = V <= kCand;                      // every token fits the list
-  const bool need_sum = !all && !by_k && (s.p < 1.0 || s.off);
+  const bool need_sum = row_needs_sum(s, V);
   count = -1;
   if (by_k && !all && s.k > kMaxListK) return false;
   float top = -INFINITY;
   uint32_t low = 0xffffffffu;
-  if (need_sum) stream_row<LT, THREADS, true>(row, V, s.c, G, gm, sh, top, low);
+  if constexpr (PRE) load_streamed<THREADS>(A, r, groups, tiles, need_sum, gm, sh, top, low);
+  else if (need_sum) stream_row<LT, THREADS, true>(row, V, s.c, G, gm, sh, top, low);
   else stream_row<LT, THREADS, false>(row, V, s.c, G, gm, sh, top, low);
   const float m = block_reduce<THREADS>(top, reinterpret_cast<float*>(sh.redi), OpMax());
   low = block_reduce<THREADS>(low, reinterpret_cast<uint32_t*>(sh.redi), OpMin());
@@ -650,16 +696,21 @@ __device__ __forceinline__ bool filter_row_list(const LT* row, int V, const Filt
     mp_key = max(mp_key, min(kmax, logit_key(clean_logit(z)) - 2));
   }
   bool complete = true;                             // the list holds every kept token
+  double got = 0.0;
+  uint32_t kprev = 0;
   for (int attempt = 0;; ++attempt) {
     uint32_t kt = kKeyNegInf + 1;
     if (!all) {
       if (by_k) {
-        kt = s.k == 1 ? kmax : threshold_key<THREADS>(gm, groups, kmax, low, m, 0.f, s.k, 0.f, sh);
+        kt = s.k == 1 ? kmax : threshold_key<THREADS>(gm, groups, kmax, low, 0, m, 0.f, s.k, 0.f, sh);
         if (s.p >= 1.0) kt = max(kt, mp_key);
       } else if (s.p < 1.0) {
-        // aim a little past the share p of the sum, further if that fell short
-        const double aim = s.p + (1.0 - s.p) * (attempt == 0 ? 0.25 : 0.75);
-        kt = threshold_key<THREADS>(gm, groups, kmax, low, m, (float)s.c, 0, (float)(aim * S), sh);
+        // the share p of the sum, as the group maxima tell it; where that fell
+        // short, the missing part (and a quarter more) from the keys below
+        const float aim = (float)(attempt == 0 ? s.p * S : 1.25 * (s.p * S - got));
+        kt = threshold_key<THREADS>(gm, groups, attempt == 0 ? kmax : kprev - 1, low,
+                                    attempt == 0 ? 0 : sh.nq, m, (float)s.c, 0, aim, sh);
+        kprev = kt;
         complete = kt <= mp_key;
         kt = max(kt, mp_key);
       } else {
@@ -718,7 +769,8 @@ __device__ __forceinline__ bool filter_row_list(const LT* row, int V, const Filt
     double run = block_scan<THREADS>(part, sh.red, total);
     const double target = s.p * (need_sum ? S : total);
     if (!complete && total < target) {
-      if (attempt) return false;
+      if (attempt == 7) return false;
+      got = total;
       continue;
     }
     int keep = 0;
@@ -823,7 +875,37 @@ __device__ __forceinline__ int draw_tiles(const LT* row, int V, RowShared<THREAD
 }
 
 // ---------------------------------------------------------------- kernels
-template <typename LT, int THREADS>
+// The stream of few rows by all CUs: one wave per tile.
+constexpr int kStreamThreads = 256;
+template <typename LT>
+__global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLaunch A) {
+  __shared__ double table[kExpTable];
+  const long r = blockIdx.x;
+  const int V = A.V, G = group_octets(V);
+  const int tiles = (V + kRowTile - 1) / kRowTile;
+  int errors = 0;
+  const FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps,
+                                           A.min_ps, (int)(r / A.per_seq), V, errors);
+  const long ri = A.row_index ? (long)A.row_index[r] : r;
+  if (ri < 0 || ri >= A.n_rows) return;
+  const LT* row = static_cast<const LT*>(A.logits) + ri * A.row_stride;
+  const bool sum = row_needs_sum(s, V);
+  if (sum) {                                        // uniform
+    fill_exp_table(table, threadIdx.x, kStreamThreads);
+    __syncthreads();
+  }
+  const int t = blockIdx.y * (kStreamThreads / kWave) + threadIdx.x / kWave;
+  if (t >= tiles) return;
+  float* gm = A.group_max + r * ((long)tiles * (8 / G) * kWave);
+  float* tm = A.tile_max + r * tiles + t;
+  double* ts = A.tile_sum + r * tiles + t;
+  float top = -INFINITY;
+  uint32_t low = 0xffffffffu;
+  if (sum) stream_tile<LT, true>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
+  else stream_tile<LT, false>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
+}
+
+template <typename LT, int THREADS, bool PRE>
 __global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
   extern __shared__ __align__(16) unsigned char lds[];
   RowShared<THREADS>& sh = *reinterpret_cast<RowShared<THREADS>*>(lds);
@@ -841,7 +923,7 @@ __global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
   int count = 0;                                    // entries in sh.list; -1: none, not a list
   bool general = false;
   if (there) {
-    general = !filter_row_list<LT, THREADS>(row, V, s, A.out_tokens || A.lists, gm, sh, f, count);
+    general = !filter_row_list<LT, THREADS, PRE>(A, r, row, V, s, A.out_tokens || A.lists, gm, sh, f, count);
     if (general) {
       __syncthreads();
       f = filter_row<LT, THREADS>(row, V, s, *reinterpret_cast<FilterShared<THREADS>*>(lds));
@@ -1015,44 +1097,95 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
 
 }  // namespace
 
-size_t filter_workspace_bytes(long n_rows, int V) {
-  (void)V;
-  return (size_t)n_rows * (sizeof(sv_filter_row) + (kCand + 4) * sizeof(int32_t));
-}
-
 namespace {
-template <typename LT, int THREADS>
+
+// Rows whose stream gets a kernel of its own, spread over all CUs.
+bool streams_apart(long rows, int V) { return V > kCand && rows <= 512; }
+
+// The parts of the workspace, in order; each starts at a multiple of 16 bytes.
+struct FilterWorkspace {
+  size_t rows = 0, counts = 0, lists = 0, group_max = 0, tile_max = 0, tile_sum = 0, bytes = 0;
+  FilterWorkspace(long n, int V, bool verify) {
+    const size_t tiles = (V + kRowTile - 1) / kRowTile;
+    size_t at = 0;
+    const auto part = [&](size_t& where, size_t size) {
+      where = at;
+      at += (size + 15) / 16 * 16;
+    };
+    if (verify) {
+      part(rows, n * sizeof(sv_filter_row));
+      part(counts, n * sizeof(int32_t));
+      part(lists, n * kCand * sizeof(int32_t));
+    }
+    if (streams_apart(n, V)) {
+      part(group_max, n * tiles * (8 / group_octets(V)) * kWave * sizeof(float));
+      part(tile_max, n * tiles * sizeof(float));
+      part(tile_sum, n * tiles * sizeof(double));
+    }
+    bytes = at;
+  }
+};
+
+template <typename LT, int THREADS, bool PRE>
 void launch_rows(const FilterLaunch& L, hipStream_t stream) {
   const int tiles = (L.V + kRowTile - 1) / kRowTile;
   const size_t gm = (size_t)tiles * (8 / group_octets(L.V)) * kWave * sizeof(float);
   const size_t lds = std::max(sizeof(RowShared<THREADS>) + gm, sizeof(FilterShared<THREADS>));
-  filter_rows_kernel<LT, THREADS>
+  filter_rows_kernel<LT, THREADS, PRE>
       <<<dim3((unsigned)((long)L.B * L.per_seq)), THREADS, lds, stream>>>(L);
 }
+
+template <typename LT>
+hipError_t launch_filter(const FilterLaunch& L, hipStream_t stream) {
+  const long rows = (long)L.B * L.per_seq;
+  const int tiles = (L.V + kRowTile - 1) / kRowTile;
+  if (streams_apart(rows, L.V)) {
+    const int waves = kStreamThreads / kWave;
+    trace_before(stream, SV_KERNEL_FILTER_ROWS);
+    filter_stream_kernel<LT><<<dim3((unsigned)rows, (unsigned)((tiles + waves - 1) / waves)),
+                               kStreamThreads, 0, stream>>>(L);
+    trace_after(stream, SV_KERNEL_FILTER_ROWS);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    trace_before(stream, SV_KERNEL_FILTER_ROWS);
+    launch_rows<LT, 512, true>(L, stream);
+    trace_after(stream, SV_KERNEL_FILTER_ROWS);
+  } else {
+    trace_before(stream, SV_KERNEL_FILTER_ROWS);
+    launch_rows<LT, 256, false>(L, stream);
+    trace_after(stream, SV_KERNEL_FILTER_ROWS);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
-hipError_t launch_filter_rows(const FilterLaunch& L, hipStream_t stream) {
-  // one workgroup per row: a large one while rows leave CUs idle
-  const bool few = (long)L.B * L.per_seq <= 512;
-  trace_before(stream, SV_KERNEL_FILTER_ROWS);
-  if (L.bf16) {
-    if (few) launch_rows<uint16_t, 1024>(L, stream);
-    else launch_rows<uint16_t, 256>(L, stream);
-  } else {
-    if (few) launch_rows<float, 1024>(L, stream);
-    else launch_rows<float, 256>(L, stream);
+size_t filter_workspace_bytes(long n_rows, int V) {
+  return FilterWorkspace(n_rows, V, true).bytes;
+}
+
+hipError_t launch_filter_rows(const FilterLaunch& L0, hipStream_t stream) {
+  FilterLaunch L = L0;
+  char* ws = static_cast<char*>(L.workspace);
+  const FilterWorkspace at((long)L.B * L.per_seq, L.V, L.verify);
+  if (L.verify) {
+    L.out_rows = reinterpret_cast<sv_filter_row*>(ws + at.rows);
+    L.list_counts = reinterpret_cast<int32_t*>(ws + at.counts);
+    L.lists = reinterpret_cast<int32_t*>(ws + at.lists);
   }
-  trace_after(stream, SV_KERNEL_FILTER_ROWS);
-  return hipGetLastError();
+  L.group_max = reinterpret_cast<float*>(ws + at.group_max);
+  L.tile_max = reinterpret_cast<float*>(ws + at.tile_max);
+  L.tile_sum = reinterpret_cast<double*>(ws + at.tile_sum);
+  return L.bf16 ? launch_filter<uint16_t>(L, stream) : launch_filter<float>(L, stream);
 }
 
 hipError_t launch_filtered_verify(const FilteredVerifyLaunch& L0, hipStream_t stream) {
   FilteredVerifyLaunch L = L0;
-  // workspace: filter rows, kept-token counts, kept tokens
-  const long rows = (long)L.B * (L.K + 1);
-  L.rows = static_cast<sv_filter_row*>(L.workspace);
-  L.list_counts = reinterpret_cast<int32_t*>(L.rows + rows);
-  L.lists = L.list_counts + (rows + 3) / 4 * 4;
+  const FilterWorkspace at((long)L.B * (L.K + 1), L.V, true);
+  char* ws = static_cast<char*>(L.workspace);
+  L.rows = reinterpret_cast<sv_filter_row*>(ws + at.rows);
+  L.list_counts = reinterpret_cast<int32_t*>(ws + at.counts);
+  L.lists = reinterpret_cast<int32_t*>(ws + at.lists);
   FilterLaunch F{};
   F.logits = L.logits;
   F.row_stride = L.row_stride;
@@ -1066,9 +1199,8 @@ hipError_t launch_filtered_verify(const FilteredVerifyLaunch& L0, hipStream_t st
   F.per_seq = L.K + 1;
   F.V = L.V;
   F.bf16 = L.bf16;
-  F.out_rows = L.rows;
-  F.lists = L.lists;
-  F.list_counts = L.list_counts;
+  F.workspace = L.workspace;
+  F.verify = 1;
   F.device_error = L.device_error;
   hipError_t e = launch_filter_rows(F, stream);
   if (e != hipSuccess) return e;

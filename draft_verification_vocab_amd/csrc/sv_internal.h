@@ -118,9 +118,15 @@ struct FilterLaunch {
   int32_t* out_tokens;           // may be NULL, as the next two
   float* out_probs;
   sv_filter_row* out_rows;
-  int32_t* lists;                // kept tokens in vocabulary order, for the verify, or NULL
-  int32_t* list_counts;          // their number per row; -1: no list
+  void* workspace;
+  int verify;                    // filter rows and kept tokens go to the workspace, for the verify
   int32_t* device_error;         // may be NULL
+  // in the workspace, set by the launch
+  int32_t* lists;                // kept tokens in vocabulary order, or NULL
+  int32_t* list_counts;          // their number per row; -1: no list
+  float* group_max;
+  float* tile_max;
+  double* tile_sum;
 };
 
 struct FilteredVerifyLaunch {
