@@ -59,17 +59,20 @@ __device__ __forceinline__ double exp2_f64(double x) {
   return ldexp(p, (int)n);
 }
 
-// 2^x for -1000 <= x <= 0 to 2e-11, for the long sums: x = k/512 + r with
-// |r| <= 1/1024, 2^(k/512) from a table (fp64, in LDS; its exponent raised by
-// the whole part of k/512) and 2^r = 1 + r (c1 + r c2), c1 and c2 chosen for
-// the smallest largest error on that range (1.3e-11).  Adding 1.5 * 2^43 rounds
-// x to a multiple of 1/512 and leaves k in the sum's low word.  About 13
-// instructions, against more than 20 of exp2_f64, whose rounding and scaling
-// are of the slower kind.
+// 2^x for -1000 <= x <= 0 with a table: x = k/512 + r with |r| <= 1/1024,
+// 2^(k/512) from the table (fp64, in LDS; its exponent raised by the whole part
+// of k/512) and 2^r = 1 + q(r).  Adding 1.5 * 2^43 rounds x to a multiple of
+// 1/512 and leaves k in the sum's low word.  With q = r (c1 + r c2), c1 and c2
+// chosen for the smallest largest error on that range, it is exact to 1.3e-11,
+// at about 13 instructions against more than 20 of exp2_f64, whose rounding and
+// scaling are of the slower kind (for the long sums); with the exponential
+// series up to r^3 (LONG) to 1e-14.
 constexpr int kExpTable = 512;
 __device__ __forceinline__ void fill_exp_table(double* table, int t, int threads) {
+#pragma unroll 1
   for (int i = t; i < kExpTable; i += threads) table[i] = exp2_f64(i * (1.0 / kExpTable));
 }
+template <bool LONG>
 __device__ __forceinline__ double exp2_table(double x, const double* table) {
   const double y = x + 0x1.8p43;
   const uint32_t k = (uint32_t)__double_as_longlong(y);
@@ -77,6 +80,9 @@ __device__ __forceinline__ double exp2_table(double x, const double* table) {
   const unsigned long long t = __double_as_longlong(table[k & (kExpTable - 1)]);
   const uint32_t hi = (uint32_t)(t >> 32) + ((k & ~(uint32_t)(kExpTable - 1)) << 11);
   const double T = __longlong_as_double(((unsigned long long)hi << 32) | (uint32_t)t);
+  if constexpr (LONG)
+    return fma(T, r * fma(r, fma(r, 5.5504108664821580e-02, 2.4022650695910071e-01),
+                          6.9314718055994531e-01), T);
   return fma(T, r * fma(r, 0.24022651860784677, 0.6931472202592015), T);
 }
 
@@ -85,6 +91,13 @@ __device__ __forceinline__ double exp2_table(double x, const double* table) {
 __device__ __forceinline__ double weight(float z, float m, double c) {
   if (z == m) return 1.0;
   return z > -INFINITY ? exp2_f64(((double)z - (double)m) * c) : 0.0;
+}
+
+// The same with a table, to 1e-14 (0 below 2^-1000).
+__device__ __forceinline__ double weight(float z, float m, double c, const double* table) {
+  if (z == m) return 1.0;
+  const double x = ((double)z - (double)m) * c;
+  return z > -INFINITY && x > -1000.0 ? exp2_table<true>(x, table) : 0.0;
 }
 
 // Whether a filter row keeps token x of logit z (cleaned).

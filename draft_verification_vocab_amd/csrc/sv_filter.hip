@@ -119,20 +119,21 @@ __device__ __forceinline__ bool cut_keeps(const Cut& c, uint32_t key, int e) {
 
 // Index of the t-th token (t >= 1, in index order) whose key is `key`.
 template <typename LT, int THREADS>
-__device__ __forceinline__ int nth_tie(const LT* row, int V, uint32_t key, int t, FilterShared<THREADS>& sh) {
+__device__ __forceinline__ int nth_tie(const LT* row, int V, uint32_t key, int t, uint32_t* cnt,
+                                       int* slot) {
   const int tiles = (V + kDrawTile - 1) / kDrawTile;
   __syncthreads();
-  for (int i = threadIdx.x; i < tiles; i += THREADS) sh.cnt[i] = 0;
+  for (int i = threadIdx.x; i < tiles; i += THREADS) cnt[i] = 0;
   __syncthreads();
   each_logit<LT, THREADS>(row, V, [&](float z, int e) {
-    if (logit_key(z) == key) atomicAdd(&sh.cnt[e / kDrawTile], 1u);
+    if (logit_key(z) == key) atomicAdd(&cnt[e / kDrawTile], 1u);
   });
   __syncthreads();
   if (threadIdx.x < kWave) {
     const int l = lane_id();
     int tile = 0, before = 0;
     for (; tile < tiles - 1; ++tile) {
-      const int n = (int)sh.cnt[tile];
+      const int n = (int)cnt[tile];
       if (before + n >= t) break;
       before += n;
     }
@@ -150,10 +151,10 @@ __device__ __forceinline__ int nth_tie(const LT* row, int V, uint32_t key, int t
       }
       before += n;
     }
-    if (l == 0) sh.bin = found;
+    if (l == 0) *slot = found;
   }
   __syncthreads();
-  const int r = sh.bin;
+  const int r = *slot;
   __syncthreads();
   return r;
 }
@@ -266,7 +267,7 @@ __device__ __forceinline__ sv_filter_row filter_row(const LT* row, int V, const 
     const uint32_t key = radix_cut<LT, THREADS, false>(row, V, cut, m, s.c, (double)s.k, ties,
                                                        above, sh);
     const int keep = s.k - (int)above;
-    cut = Cut{key, keep >= ties ? V : nth_tie<LT, THREADS>(row, V, key, keep, sh)};
+    cut = Cut{key, keep >= ties ? V : nth_tie<LT, THREADS>(row, V, key, keep, sh.cnt, &sh.bin)};
   }
   if (s.p < 1.0) {
     double part = 0.0;
@@ -288,7 +289,7 @@ __device__ __forceinline__ sv_filter_row filter_row(const LT* row, int V, const 
     const double need = w > 0.0 ? ceil(left / w) : (double)ties;
     const int keep = need >= (double)ties ? ties : need < 1.0 ? 1 : (int)need;
     if (key > cut.key || keep < ties)
-      cut = Cut{key, keep >= ties ? V : nth_tie<LT, THREADS>(row, V, key, keep, sh)};
+      cut = Cut{key, keep >= ties ? V : nth_tie<LT, THREADS>(row, V, key, keep, sh.cnt, &sh.bin)};
   }
   if (s.mp > 0.0) {
     uint32_t lk = 0xffffffffu;
@@ -338,9 +339,11 @@ constexpr int kRowTile = 4096;
 constexpr int kRowTiles = SV_MAX_V / kRowTile;
 constexpr int kCand = 2048;            // candidate tokens a workgroup sorts in LDS
 constexpr int kQueue = 2048;           // candidate groups
-constexpr int kTopBins = 512;          // histogram of the group maxima
+constexpr int kTopBins = 256;          // histogram of the group maxima
+constexpr int kFirst = 96;             // groups whose tokens a nucleus row looks at first
+constexpr int kGeneralRow = -2;        // list_counts: the row takes the general path
 constexpr int kMaxListK = 1024;        // largest top-k taken through the candidate list
-constexpr int kRankN = 256;            // most entries sorted by counting
+constexpr int kRankN = 512;            // most entries sorted by counting
 
 // Octets per group: 8, or fewer as long as there are at most 3200 groups.
 __host__ __device__ __forceinline__ int group_octets(int V) {
@@ -350,11 +353,11 @@ __host__ __device__ __forceinline__ int group_octets(int V) {
 
 template <int THREADS>
 struct RowShared {
-  unsigned long long list[kCand];      // candidates
+  unsigned long long list[kCand];      // candidates: order_entry
   union {
     struct { uint32_t cnt[kTopBins], mass[kTopBins]; } top;
     uint16_t queue[kQueue];
-    unsigned long long sorted[kRankN];
+    unsigned long long bucket[256];
   };
   double tile_s[kRowTiles];
   float tile_m[kRowTiles];
@@ -371,19 +374,29 @@ __device__ __forceinline__ void sort_list(RowShared<THREADS>& sh, int n) {
   __syncthreads();
   if (n <= kRankN) {
     // each entry's place is the number of smaller ones (no two are equal)
-    const int i = threadIdx.x;
-    unsigned long long x = 0;
-    int rank = 0;
-    if (i < n) {
-      x = sh.list[i];
-      for (int j = 0; j < n; ++j) rank += sh.list[j] < x;
+    constexpr int PER = (kRankN + THREADS - 1) / THREADS;
+    unsigned long long x[PER];
+    int rank[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int i = p * THREADS + threadIdx.x;
+      x[p] = i < n ? sh.list[i] : 0;
+      rank[p] = 0;
+    }
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const unsigned long long y = sh.list[j];
+#pragma unroll
+      for (int p = 0; p < PER; ++p) rank[p] += y < x[p];
     }
     __syncthreads();
-    if (i < n) sh.list[rank] = x;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (p * THREADS + (int)threadIdx.x < n) sh.list[rank[p]] = x[p];
     __syncthreads();
     return;
   }
-  int N = 512;
+  int N = 2 * kRankN;
   while (N < n) N <<= 1;
   for (int i = n + threadIdx.x; i < N; i += THREADS) sh.list[i] = ~0ull;
   for (int size = 2; size <= N; size <<= 1)
@@ -421,52 +434,62 @@ __device__ __forceinline__ unsigned long long order_entry(uint32_t key, int e) {
   return ((unsigned long long)~key << 32) | (uint32_t)e;
 }
 
-// One wave's tile t of a row: its groups' maxima to gm (the row's), with SUM
+// Whether a row's filters need the sum of all its weights: no top-k bounds the
+// tokens that matter, and they do not all fit the candidate list.
+__device__ __forceinline__ bool row_needs_sum(const FilterSettings& s, int V) {
+  return V > kCand && s.k >= V && (s.p < 1.0 || s.off);
+}
+// How the stream takes it.
+enum RowSum { NO_SUM, SUM_F32, SUM_F64 };
+
+// One wave's tile t of a row: its groups' maxima to gm (the row's), with a sum
 // its maximum and sum of weights to *tile_m, *tile_s.  Gives the lane's largest
-// logit and its groups' lowest key above -inf.
-template <typename LT, bool SUM>
+// logit and its groups' lowest key above -inf.  128 bytes a lane are in flight:
+// a bf16 tile at once, an fp32 tile in two parts.
+template <typename LT, RowSum SUM>
 __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double c, int G, float* gm,
                                             float* tile_m, double* tile_s, const double* table,
                                             float& top, uint32_t& low) {
+  constexpr int OCTS = 16 / sizeof(LT);
   const int l = lane_id();
   const int per = 8 / G;
-  {
-    Raw<LT> raw[8];
-    const int e0 = t * kRowTile + 8 * l;
+  float g = -INFINITY, ref = -INFINITY;             // ref: the sum's reference logit
+  double sum = 0.0;
+#pragma unroll 1
+  for (int part = 0; part < 8 / OCTS; ++part) {
+    Raw<LT> raw[OCTS];
+    const int e0 = t * kRowTile + part * OCTS * kTile + 8 * l;
     if ((t + 1) * kRowTile <= V) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) raw8(row + e0 + u * kTile, raw[u]);
+      for (int u = 0; u < OCTS; ++u) raw8(row + e0 + u * kTile, raw[u]);
     } else {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < OCTS; ++u) {
         const int e = e0 + u * kTile;
         if (e + 8 <= V) raw8(row + e, raw[u]);
         else raw8_end(row, e, V, raw[u]);
       }
     }
-    float om[8];
+    float mt = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < OCTS; ++u) {
       float z[8];
       unpack(raw[u], z);
-      om[u] = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])),
-                    fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
-    }
-    float mt = -INFINITY;
-    float g = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      g = fmaxf(g, om[u]);
-      if (((u + 1) & (G - 1)) == 0) {               // uniform
+      g = fmaxf(g, fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])),
+                         fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7]))));
+      if (((u + 1) & (G - 1)) == 0 || u + 1 == OCTS) {   // uniform
         g = clean_logit(g);
-        gm[(t * per + u / G) * kWave + l] = g;
-        if (g > -INFINITY) low = min(low, logit_key(g));
         mt = fmaxf(mt, g);
-        g = -INFINITY;
+        const int o = part * OCTS + u + 1;
+        if ((o & (G - 1)) == 0) {                   // a group ends
+          gm[(t * per + (o - 1) / G) * kWave + l] = g;
+          if (g > -INFINITY) low = min(low, logit_key(g));
+          g = -INFINITY;
+        }
       }
     }
     top = fmaxf(top, mt);
-    if constexpr (SUM) {
+    if constexpr (SUM != NO_SUM) {
       mt = wave_max(mt);
       double s = 0.0, s1 = 0.0;
       // Logits 500 octaves and more below the maximum (and -inf, NaN) count
@@ -474,42 +497,62 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
       // from the maximum in fp32 (huge or infinite logits, huge temperatures),
       // each weight is computed by itself.
       const float floor = (float)((double)mt - 500.0 / c);
-      if (fabs((double)mt) * c < 4096.0 && floor < mt && floor > -INFINITY) {
-        const double ref = -(double)mt * c;
+      const bool plain = fabs((double)mt) * c < 4096.0 && floor < mt && floor > -INFINITY;
+      if (SUM == SUM_F32 && plain) {
+        // z - mt is exact for bf16 logits (2^-24 relative for fp32 ones), the
+        // product with c off by 2^-23 |x| in all, the exponential by 2^-23
+        // relative: a term is exact to (0.7 |x| + 1) 2^-23.  Eight terms are
+        // added in fp32, then in fp64.
+        const float c32 = (float)c;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < OCTS; ++u) {
+          keep_raw(raw[u]);
+          float z[8], e[8];
+          unpack(raw[u], z);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            e[j] = __builtin_amdgcn_exp2f((fmaxf(z[j], floor) - mt) * c32);
+          s += (double)tree_sum8(e);
+          __builtin_amdgcn_sched_barrier(0);        // one octet in flight: registers
+        }
+      } else if (plain) {
+        const double shift = -(double)mt * c;
+#pragma unroll
+        for (int u = 0; u < OCTS; ++u) {
           keep_raw(raw[u]);
           float z[8];
           unpack(raw[u], z);
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            s += exp2_table(fma((double)fmaxf(z[j], floor), c, ref), table);
-            s1 += exp2_table(fma((double)fmaxf(z[j + 1], floor), c, ref), table);
+            s += exp2_table<false>(fma((double)fmaxf(z[j], floor), c, shift), table);
+            s1 += exp2_table<false>(fma((double)fmaxf(z[j + 1], floor), c, shift), table);
           }
-          __builtin_amdgcn_sched_barrier(0);        // one octet in flight: registers
+          __builtin_amdgcn_sched_barrier(0);
         }
       } else if (mt > -INFINITY) {
 #pragma unroll 1
-        for (int i = 0; i < kRowTile / kWave; ++i) {
-          const int e = t * kRowTile + i * kWave + l;
-          if (e < V) s += weight(clean_logit(logit_at(row, e)), mt, c);
+        for (int i = 0; i < OCTS * 8; ++i) {
+          const int e = t * kRowTile + part * OCTS * kTile + i * kWave + l;
+          if (e < V) s += weight(clean_logit(logit_at(row, e)), mt, c, table);
         }
       }
       s = wave_sum(s + s1);
-      if (l == 0) { *tile_m = mt; *tile_s = s; }
+      if (mt > ref) {
+        sum *= ref > -INFINITY ? weight(ref, mt, c, table) : 0.0;
+        ref = mt;
+      }
+      if (mt > -INFINITY) sum += s * weight(mt, ref, c, table);
     }
   }
+  if constexpr (SUM != NO_SUM)
+    if (l == 0) { *tile_m = ref; *tile_s = sum; }
 }
 
 // A whole row by one workgroup, into LDS.
-template <typename LT, int THREADS, bool SUM>
+template <typename LT, int THREADS, RowSum SUM>
 __device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G, float* gm,
                                            RowShared<THREADS>& sh, float& top, uint32_t& low) {
   const int tiles = (V + kRowTile - 1) / kRowTile;
-  if constexpr (SUM) {
-    fill_exp_table(sh.table, threadIdx.x, THREADS);
-    __syncthreads();
-  }
   for (int t = threadIdx.x / kWave; t < tiles; t += THREADS / kWave)
     stream_tile<LT, SUM>(row, V, t, c, G, gm, &sh.tile_m[t], &sh.tile_s[t], sh.table, top, low);
 }
@@ -534,8 +577,8 @@ __device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int
 }
 
 // The key from which on logits can be kept, from the group maxima: at least k
-// of them reach it (by count), or about `share` of the row's sum S lies in
-// logits that reach it (by mass).  Histograms of the maxima's keys, the first
+// of them reach it (by count, k > 0), or the weights of the logits that do are
+// about `aim` times that of logit z0 (by mass, k = 0).  Histograms of the maxima's keys, the first
 // over their whole range, then over the bin of the threshold while that bin is
 // wide.  A maximum stands for the group's tokens of its own size; in the
 // estimate of the mass, those hidden behind a larger one of their group are
@@ -543,11 +586,11 @@ __device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int
 // key `hi`, `above` groups lying above it.
 template <int THREADS>
 __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, uint32_t hi,
-                                                  uint32_t lo, int above, float m, float c, int k,
-                                                  float share_mass, RowShared<THREADS>& sh) {
+                                                  uint32_t lo, int above, float z0, float c, int k,
+                                                  float aim, RowShared<THREADS>& sh) {
   const bool by_mass = k == 0;
   if (hi < lo) return kKeyNegInf + 1;
-  float mass = 0.f;                    // estimated mass found, in units of the maximum
+  float mass = 0.f;                    // estimated mass found
 #pragma unroll 1
   for (int level = 0; level < 4; ++level) {
     int shift = 0;
@@ -565,7 +608,7 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
         atomicAdd(&sh.top.cnt[b], 1u);
         if (by_mass)
           atomicAdd(&sh.top.mass[b],
-                    g == m ? 262144u : (uint32_t)(__builtin_amdgcn_exp2f((g - m) * c) * 262144.f));
+                    g >= z0 ? 262144u : (uint32_t)(__builtin_amdgcn_exp2f((g - z0) * c) * 262144.f));
       }
     }
     __syncthreads();
@@ -591,12 +634,19 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
           run += n[i];
         }
       } else {
-        float f[PER], fmine = 0.f;
+        // elements per group maximum of a bin: at most groups / (groups not
+        // yet reached at its end); over the whole bin the logarithm's mean
+        float f[PER], most[PER], fmine = 0.f;
         int r = run;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          f[i] = (float)sh.top.mass[l * PER + i] * (1.f / 262144.f) *
-                 ((float)groups * __builtin_amdgcn_rcpf((float)max(1, groups - r)));
+          const float x = (float)sh.top.mass[l * PER + i] * (1.f / 262144.f) * (float)groups;
+          const float left = (float)max(1, groups - r), after = (float)max(1, groups - r - n[i]);
+          most[i] = x * __builtin_amdgcn_rcpf(after);
+          f[i] = n[i] ? x * 0.69314718f *
+                            __builtin_amdgcn_logf(left * __builtin_amdgcn_rcpf(after)) *
+                            __builtin_amdgcn_rcpf((float)n[i])
+                      : 0.f;
           r += n[i];
           fmine += f[i];
         }
@@ -609,7 +659,7 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
         frun += mass - fmine;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          if (hit < 0 && n[i] && frun + f[i] >= share_mass) {
+          if (hit < 0 && n[i] && frun + most[i] >= aim) {
             hit = l * PER + i; before = run; fbefore = frun;
           }
           run += n[i];
@@ -623,7 +673,9 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
     }
     __syncthreads();
     const int b = sh.bin;
-    if (b < 0) return kKeyNegInf + 1;               // not reached: every token
+    // not reached: every token, or (by mass, inside a bin that seemed to reach
+    // it) what there is
+    if (b < 0) return level == 0 ? kKeyNegInf + 1 : lo;
     above = sh.above;
     mass = sh.frac;
     const int in = (int)sh.top.cnt[b];
@@ -637,192 +689,268 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
   return lo;
 }
 
-// Whether a row's filters need the sum of all its weights: no top-k bounds the
-// tokens that matter, and they do not all fit the candidate list.
-__device__ __forceinline__ bool row_needs_sum(const FilterSettings& s, int V) {
-  return V > kCand && s.k >= V && (s.p < 1.0 || s.off);
+// The tokens whose logit is at least zt into sh.list, in any order.  Returns their number, or -1 if they or their groups
+// are more than the lists hold.
+template <typename LT, int THREADS>
+__device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int groups,
+                                             const float* gm, float zt,
+                                             RowShared<THREADS>& sh) {
+  const int per = 8 / G;
+  __syncthreads();
+  if (threadIdx.x == 0) { sh.nq = 0; sh.n = 0; }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < groups; i += THREADS)
+    if (gm[i] >= zt) {
+      const int q = atomicAdd(&sh.nq, 1);
+      if (q < kQueue) sh.queue[q] = (uint16_t)i;
+    }
+  __syncthreads();
+  const int nq = sh.nq;
+  if (nq > kQueue) return -1;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < nq * G; i += THREADS) {
+    const int q = sh.queue[i / G], u = q / kWave % per * G + i % G;
+    const int e = q / (per * kWave) * kRowTile + u * kTile + q % kWave * 8;
+    float z[8];
+    if (e + 8 <= V) {
+      load8(row + e, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = e + j < V ? logit_at(row, e + j) : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = clean_logit(z[j]);
+      if (x >= zt) {
+        const int at = atomicAdd(&sh.n, 1);
+        if (at < kCand) sh.list[at] = order_entry(logit_key(x), e + j);
+      }
+    }
+  }
+  __syncthreads();
+  return sh.n > kCand ? -1 : sh.n;
 }
 
 // The kept set of one row through the candidate list.  Returns false where the
 // row has to take the general path (filter_row): more candidates than the list
-// holds, or a large top-k.  `order` asks for the kept
-// tokens in vocabulary order: entries (index, key) in sh.list[0 .. count).
+// holds, or a large top-k.  The kept tokens are in sh.list[0 .. count), in any
+// order; count is -1 for rows without a list.
 template <typename LT, int THREADS, bool PRE>
-__device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, const LT* row, int V, const FilterSettings& s, bool order, float* gm,
-                                RowShared<THREADS>& sh, sv_filter_row& f, int& count) {
-  const int G = group_octets(V), per = 8 / G;
+__device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, const LT* row, int V,
+                                                const FilterSettings& s, float* gm,
+                                                RowShared<THREADS>& sh, sv_filter_row& f,
+                                                int& count) {
+  const int G = group_octets(V);
   const int tiles = (V + kRowTile - 1) / kRowTile;
-  const int groups = tiles * per * kWave;
+  const int groups = tiles * (8 / G) * kWave;
   const bool by_k = s.k < V;
   const bool all = V <= kCand;                      // every token fits the list
   const bool need_sum = row_needs_sum(s, V);
+  const bool nucleus = need_sum && !s.off;
   count = -1;
   if (by_k && !all && s.k > kMaxListK) return false;
-  float top = -INFINITY;
-  uint32_t low = 0xffffffffu;
-  if constexpr (PRE) load_streamed<THREADS>(A, r, groups, tiles, need_sum, gm, sh, top, low);
-  else if (need_sum) stream_row<LT, THREADS, true>(row, V, s.c, G, gm, sh, top, low);
-  else stream_row<LT, THREADS, false>(row, V, s.c, G, gm, sh, top, low);
-  const float m = block_reduce<THREADS>(top, reinterpret_cast<float*>(sh.redi), OpMax());
-  low = block_reduce<THREADS>(low, reinterpret_cast<uint32_t*>(sh.redi), OpMin());
-  f = sv_filter_row{s.c, 0.0, m, INFINITY, -1, 0};
-  if (m == -INFINITY) { count = 0; return true; }
-  double S = 0.0;
-  if (need_sum) {
-    double part = 0.0;
+  // The sum of a nucleus row is first taken in fp32 (unless a kernel of its own
+  // took it in fp64), and again in fp64 where its error could move the cut.
 #pragma unroll 1
-    for (int t = threadIdx.x; t < tiles; t += THREADS) {
-      const double x = sh.tile_m[t] > -INFINITY
-                           ? sh.tile_s[t] * weight(sh.tile_m[t], m, s.c) : 0.0;
-      sh.tile_s[t] = x;
-      part += x;
+  for (bool exact = PRE || !nucleus;; exact = true) {
+    float top = -INFINITY;
+    uint32_t low = 0xffffffffu;
+    if constexpr (PRE) load_streamed<THREADS>(A, r, groups, tiles, need_sum, gm, sh, top, low);
+    else if (!need_sum) stream_row<LT, THREADS, NO_SUM>(row, V, s.c, G, gm, sh, top, low);
+    else if (exact) stream_row<LT, THREADS, SUM_F64>(row, V, s.c, G, gm, sh, top, low);
+    else stream_row<LT, THREADS, SUM_F32>(row, V, s.c, G, gm, sh, top, low);
+    const float m = block_reduce<THREADS>(top, reinterpret_cast<float*>(sh.redi), OpMax());
+    low = block_reduce<THREADS>(low, reinterpret_cast<uint32_t*>(sh.redi), OpMin());
+    f = sv_filter_row{s.c, 0.0, m, INFINITY, -1, 0};
+    if (m == -INFINITY) { count = 0; return true; }
+    double S = 0.0;                                 // the sum of all weights
+    if (need_sum) {
+      double part = 0.0;
+#pragma unroll 1
+      for (int t = threadIdx.x; t < tiles; t += THREADS) {
+        const double x = sh.tile_m[t] > -INFINITY
+                             ? sh.tile_s[t] * weight(sh.tile_m[t], m, s.c, sh.table) : 0.0;
+        sh.tile_s[t] = x;
+        part += x;
+      }
+      S = block_reduce<THREADS>(part, sh.red, OpAdd());
+      if (s.off) {
+        f.inv_sum = 1.0 / S;
+        f.min_kept = -INFINITY;
+        f.last = V - 1;
+        f.n_kept = V;
+        return true;
+      }
     }
-    S = block_reduce<THREADS>(part, sh.red, OpAdd());
-    if (s.off) {
-      f.inv_sum = 1.0 / S;
-      f.min_kept = -INFINITY;
-      f.last = V - 1;
-      f.n_kept = V;
-      return true;
+    // the lowest key a kept token can have
+    const uint32_t kmax = logit_key(m);
+    uint32_t mp_key = kKeyNegInf + 1;
+    if (s.mp > 0.0 && s.c > 0.0) {
+      // z >= m + log2(min_p) / c, a little lower: the exact test follows
+      const float z =
+          (float)((double)m + ((double)__builtin_amdgcn_logf((float)s.mp) - 1e-4) / s.c);
+      mp_key = max(mp_key, min(kmax, logit_key(clean_logit(z)) - 2));
     }
-  }
-
-  // the lowest key a kept token can have
-  const uint32_t kmax = logit_key(m);
-  uint32_t mp_key = kKeyNegInf + 1;
-  if (s.mp > 0.0 && s.c > 0.0) {
-    // z >= m + log2(min_p) / c, a little lower: the exact test follows
-    const float z = (float)((double)m + ((double)__builtin_amdgcn_logf((float)s.mp) - 1e-4) / s.c);
-    mp_key = max(mp_key, min(kmax, logit_key(clean_logit(z)) - 2));
-  }
-  bool complete = true;                             // the list holds every kept token
-  double got = 0.0;
-  uint32_t kprev = 0;
-  for (int attempt = 0;; ++attempt) {
+    bool complete = true;                           // the list holds every kept token
+    bool ambiguous = false;
+    double got = 0.0;
     uint32_t kt = kKeyNegInf + 1;
-    if (!all) {
-      if (by_k) {
-        kt = s.k == 1 ? kmax : threshold_key<THREADS>(gm, groups, kmax, low, 0, m, 0.f, s.k, 0.f, sh);
-        if (s.p >= 1.0) kt = max(kt, mp_key);
-      } else if (s.p < 1.0) {
-        // the share p of the sum, as the group maxima tell it; where that fell
-        // short, the missing part (and a quarter more) from the keys below
-        const float aim = (float)(attempt == 0 ? s.p * S : 1.25 * (s.p * S - got));
-        kt = threshold_key<THREADS>(gm, groups, attempt == 0 ? kmax : kprev - 1, low,
-                                    attempt == 0 ? 0 : sh.nq, m, (float)s.c, 0, aim, sh);
-        kprev = kt;
-        complete = kt <= mp_key;
-        kt = max(kt, mp_key);
-      } else {
-        kt = mp_key;
-      }
-    }
-    // candidate groups, then their tokens
-    __syncthreads();
-    if (threadIdx.x == 0) { sh.nq = 0; sh.n = 0; }
-    __syncthreads();
-    const float zt = key_logit(kt);
 #pragma unroll 1
-    for (int i = threadIdx.x; i < groups; i += THREADS)
-      if (gm[i] >= zt) {
-        const int q = atomicAdd(&sh.nq, 1);
-        if (q < kQueue) sh.queue[q] = (uint16_t)i;
-      }
-    __syncthreads();
-    const int nq = sh.nq;
-    if (nq > kQueue) return false;
-#pragma unroll 1
-    for (int i = threadIdx.x; i < nq * G; i += THREADS) {
-      const int q = sh.queue[i / G], u = q / kWave % per * G + i % G;
-      const int e = q / (per * kWave) * kRowTile + u * kTile + q % kWave * 8;
-      float z[8];
-      if (e + 8 <= V) {
-        load8(row + e, z);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = e + j < V ? logit_at(row, e + j) : -INFINITY;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = clean_logit(z[j]);
-        if (x >= zt) {
-          const int at = atomicAdd(&sh.n, 1);
-          if (at < kCand) sh.list[at] = order_entry(logit_key(x), e + j);
+    for (int attempt = 0;; ++attempt) {
+      if (!all) {
+        if (by_k || nucleus) {
+          // A nucleus row starts with the tokens of its kFirst largest groups,
+          // whose weights are then known exactly (two of the largest may share
+          // a group); what they lack of the share p, and a tenth more, is
+          // estimated from the group maxima below.
+          const bool est = nucleus && attempt > 0;
+          const int k = est ? 0 : nucleus ? min(kFirst, groups) : s.k;
+          const float z0 = est ? key_logit(kt) : m;
+          const float aim =
+              est ? (float)(1.1 * (s.p * S - got) / weight(z0, m, s.c, sh.table)) : 0.f;
+          kt = s.k == 1 ? kmax
+                        : threshold_key<THREADS>(gm, groups, est ? kt - 1 : kmax, low,
+                                                 est ? sh.nq : 0, z0, (float)s.c, k, aim, sh);
+          complete = !nucleus || kt <= mp_key;
+          if (nucleus || s.p >= 1.0) kt = max(kt, mp_key);
+        } else {
+          kt = mp_key;
         }
       }
+      const int n = gather_tokens<LT, THREADS>(row, V, G, groups, gm, key_logit(kt), sh);
+      if (n < 0) return false;
+      sort_list<THREADS>(sh, n);
+
+      // top-k, top-p and min-p along the order
+      const int nk = by_k ? min(n, s.k) : n;
+      const int chunk = (nk + THREADS - 1) / THREADS;
+      const int r0 = min((int)threadIdx.x * chunk, nk), r1 = min(r0 + chunk, nk);
+      const auto weight_of = [&](int i) {
+        return weight(key_logit(~(uint32_t)(sh.list[i] >> 32)), m, s.c, sh.table);
+      };
+      double part = 0.0, total;
+#pragma unroll 1
+      for (int i = r0; i < r1; ++i) part += weight_of(i);
+      double run = block_scan<THREADS>(part, sh.red, total);
+      const double target = s.p * (need_sum ? S : total);
+      // The fp32 sum's error: 2^-19 covers terms of |x| < 20; those below weigh
+      // under 2^-20.
+      const double slack = exact ? 0.0 : target * 0x1p-19;
+      if (!complete && total < target + slack) {
+        if (attempt == 7) return false;
+        got = total;
+        continue;
+      }
+      int keep = 0, most = 0;
+      part = 0.0;
+#pragma unroll 1
+      for (int i = r0; i < r1; ++i) {
+        const double w = weight_of(i);
+        if (w >= s.mp) {
+          if (s.p >= 1.0 || run < target - slack) { ++keep; part += w; }
+          if (s.p >= 1.0 || run < target + slack) ++most;
+        }
+        run += w;
+      }
+      // both are at most kCand
+      const int both = block_reduce<THREADS>(most << 16 | keep, sh.redi, OpAdd());
+      keep = both & 0xffff;
+      ambiguous = keep != both >> 16;
+      if (ambiguous) break;
+      f.inv_sum = 1.0 / block_reduce<THREADS>(part, sh.red, OpAdd());
+      const unsigned long long last = sh.list[keep - 1];
+      f.min_kept = s.off ? -INFINITY : key_logit(~(uint32_t)(last >> 32));
+      f.last = s.off ? V - 1 : (int)(uint32_t)last;
+      f.n_kept = s.off ? V : keep;
+      count = keep;
+      return true;
     }
     __syncthreads();
-    const int n = sh.n;
-    if (n > kCand) return false;
-    sort_list<THREADS>(sh, n);
-
-    // top-k, top-p and min-p along the order
-    const int nk = by_k ? min(n, s.k) : n;
-    const int chunk = (nk + THREADS - 1) / THREADS;
-    const int r0 = min((int)threadIdx.x * chunk, nk), r1 = min(r0 + chunk, nk);
-    const auto weight_of = [&](int r) {
-      return weight(key_logit(~(uint32_t)(sh.list[r] >> 32)), m, s.c);
-    };
-    double part = 0.0, total;
-#pragma unroll 1
-    for (int r = r0; r < r1; ++r) part += weight_of(r);
-    double run = block_scan<THREADS>(part, sh.red, total);
-    const double target = s.p * (need_sum ? S : total);
-    if (!complete && total < target) {
-      if (attempt == 7) return false;
-      got = total;
-      continue;
-    }
-    int keep = 0;
-    part = 0.0;
-#pragma unroll 1
-    for (int r = r0; r < r1; ++r) {
-      const double w = weight_of(r);
-      if ((s.p >= 1.0 || run < target) && w >= s.mp) { ++keep; part += w; }
-      run += w;
-    }
-    keep = block_reduce<THREADS>(keep, sh.redi, OpAdd());
-    f.inv_sum = 1.0 / block_reduce<THREADS>(part, sh.red, OpAdd());
-    const unsigned long long last = sh.list[keep - 1];
-    f.min_kept = s.off ? -INFINITY : key_logit(~(uint32_t)(last >> 32));
-    f.last = s.off ? V - 1 : (int)(uint32_t)last;
-    f.n_kept = s.off ? V : keep;
-    count = keep;
-    if (order) {
-      __syncthreads();
-      for (int r = threadIdx.x; r < keep; r += THREADS) {
-        const unsigned long long x = sh.list[r];
-        sh.list[r] = (x << 32) | (uint32_t)~(x >> 32);
-      }
-      sort_list<THREADS>(sh, keep);
-    }
-    return true;
   }
 }
 
-// The token drawn with uniform u from `count` entries in vocabulary order.
-template <int THREADS>
-__device__ __forceinline__ int draw_list(RowShared<THREADS>& sh, int count, float u, float m, double c) {
-  const int chunk = (count + THREADS - 1) / THREADS;
-  const int r0 = min((int)threadIdx.x * chunk, count), r1 = min(r0 + chunk, count);
-  double part = 0.0, total;
-#pragma unroll 1
-  for (int r = r0; r < r1; ++r) part += weight(key_logit((uint32_t)sh.list[r]), m, c);
-  double run = block_scan<THREADS>(part, sh.red, total);
-  const double target = (double)u * total;
-  int first = INT32_MAX, any = -1;
-#pragma unroll 1
-  for (int r = r0; r < r1; ++r) {
-    const double w = weight(key_logit((uint32_t)sh.list[r]), m, c);
-    run += w;
-    if (w > 0.0) {
-      any = r;
-      if (run > target) first = min(first, r);
+// The token drawn with uniform u from n <= N * THREADS entries in any order,
+// entry(i, token, mass).  The masses become integers, 2^50 to 2^51 the largest
+// (so that up to 4096 of them fit 64 bits and their sums do not depend on the
+// order of the additions); the token is found digit by digit, 8, 8 and 3 bits,
+// from the masses' sums per digit.  -1 if no entry has mass.  UNIT: the largest
+// mass is 1.
+template <int THREADS, int N, bool UNIT, typename F>
+__device__ __forceinline__ int draw_entries(int n, float u, unsigned long long* bucket, double* red,
+                                            F entry) {
+  static_assert(N * THREADS <= 4096, "sums fit 64 bits");
+  int id[N];
+  unsigned long long mass[N];
+  if constexpr (UNIT) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      id[j] = 0;
+      double x = 0.0;
+      if (j * THREADS + (int)threadIdx.x < n) entry(j * THREADS + threadIdx.x, id[j], x);
+      mass[j] = (unsigned long long)rint(x * 0x1p50);
     }
+    __syncthreads();
+  } else {
+    double x[N], mx = 0.0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      id[j] = 0;
+      x[j] = 0.0;
+      if (j * THREADS + (int)threadIdx.x < n) entry(j * THREADS + threadIdx.x, id[j], x[j]);
+      mx = fmax(mx, x[j]);
+    }
+    mx = block_reduce<THREADS>(mx, red, OpMax());
+    if (!(mx > 0.0)) return -1;
+    const int up = 50 - ilogb(mx);
+#pragma unroll
+    for (int j = 0; j < N; ++j) mass[j] = (unsigned long long)rint(ldexp(x[j], up));
   }
-  first = block_reduce<THREADS>(first, sh.redi, OpMin());
-  any = block_reduce<THREADS>(any, sh.redi, OpMax());
-  return (int)(sh.list[first == INT32_MAX ? any : first] >> 32);
+  int prefix = 0;
+  double target = 0.0;                              // less what lies before the prefix
+  bool last = false;                                // rounding left no crossing
+#pragma unroll
+  for (int level = 0; level < 3; ++level) {
+    const int shift = level == 0 ? 11 : level == 1 ? 3 : 0;
+    const int bits = level == 2 ? 3 : 8;
+    for (int i = threadIdx.x; i < 256; i += THREADS) bucket[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (mass[j] && (id[j] >> (shift + bits)) == prefix)
+        atomicAdd(&bucket[(id[j] >> shift) & ((1 << bits) - 1)], mass[j]);
+    __syncthreads();
+    // every wave finds the same bucket
+    const int l = lane_id();
+    unsigned long long m[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { m[i] = bucket[l * 4 + i]; mine += m[i]; }
+    unsigned long long run = mine;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const unsigned long long y = __shfl_up(run, off);
+      if (l >= off) run += y;
+    }
+    if (level == 0) target = (double)u * (double)__shfl(run, kWave - 1);
+    run -= mine;
+    int hit = -1, any = -1;
+    unsigned long long before = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (m[i]) {
+        any = l * 4 + i;
+        if (hit < 0 && !last && (double)(run + m[i]) > target) { hit = l * 4 + i; before = run; }
+      }
+      run += m[i];
+    }
+    const unsigned long long hits = __ballot(hit >= 0), anys = __ballot(any >= 0);
+    last = last || !hits;
+    const int src = hits ? __ffsll((long long)hits) - 1 : 63 - __clzll((long long)anys);
+    prefix = prefix << bits | __shfl(hits ? hit : any, src);
+    target -= (double)__shfl(before, src);
+    __syncthreads();
+  }
+  return prefix;
 }
 
 // The token drawn from a row without filters, whose tile masses stream_row
@@ -860,7 +988,7 @@ __device__ __forceinline__ int draw_tiles(const LT* row, int V, RowShared<THREAD
 #pragma unroll 1
     for (int i = 0; i < kRowTile / kWave && token < 0; ++i) {
       const int e0 = tile * kRowTile + i * kWave, e = e0 + l;
-      const double y = e < V ? weight(clean_logit(logit_at(row, e)), m, c) : 0.0;
+      const double y = e < V ? weight(clean_logit(logit_at(row, e)), m, c, sh.table) : 0.0;
       const double in = wave_inclusive_scan(y);
       const unsigned long long pos = __ballot(y > 0.0);
       if (pos) lastpos = e0 + 63 - __clzll((long long)pos);
@@ -901,8 +1029,8 @@ __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLau
   double* ts = A.tile_sum + r * tiles + t;
   float top = -INFINITY;
   uint32_t low = 0xffffffffu;
-  if (sum) stream_tile<LT, true>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
-  else stream_tile<LT, false>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
+  if (sum) stream_tile<LT, SUM_F64>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
+  else stream_tile<LT, NO_SUM>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
 }
 
 template <typename LT, int THREADS, bool PRE>
@@ -920,38 +1048,37 @@ __global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
   const bool there = ri >= 0 && ri < A.n_rows;
   sv_filter_row f{0.0, 0.0, -INFINITY, INFINITY, -1, 0};
   const LT* row = static_cast<const LT*>(A.logits) + (there ? ri : 0) * A.row_stride;
-  int count = 0;                                    // entries in sh.list; -1: none, not a list
-  bool general = false;
-  if (there) {
-    general = !filter_row_list<LT, THREADS, PRE>(A, r, row, V, s, A.out_tokens || A.lists, gm, sh, f, count);
-    if (general) {
-      __syncthreads();
-      f = filter_row<LT, THREADS>(row, V, s, *reinterpret_cast<FilterShared<THREADS>*>(lds));
-      count = -1;
-    }
+  fill_exp_table(sh.table, threadIdx.x, THREADS);
+  __syncthreads();
+  int count = 0;                                    // entries in sh.list; -1: no list
+  if (there && !filter_row_list<LT, THREADS, PRE>(A, r, row, V, s, gm, sh, f, count)) {
+    if (threadIdx.x == 0) A.list_counts[r] = kGeneralRow;
+    return;
   }
   if (!there) errors |= SV_DEVERR_ROW_INDEX;
   else if (f.n_kept == 0) errors |= SV_DEVERR_EMPTY_ROW;
   if (threadIdx.x == 0) {
     if (errors) flag_error(A.device_error, errors);
     if (A.out_rows) A.out_rows[r] = f;
-    if (A.lists) A.list_counts[r] = count;
+    if (A.list_counts) A.list_counts[r] = count;
   }
   if (A.lists)
     for (int i = threadIdx.x; i < count; i += THREADS)
-      A.lists[r * kCand + i] = (int32_t)(sh.list[i] >> 32);
+      A.lists[r * kCand + i] = (int32_t)(uint32_t)sh.list[i];
   if (A.out_tokens) {
     int token = there ? 0 : -1;
     if (f.n_kept > 0) {
       if (s.c == 0.0) token = f.last;
-      else if (count > 0) token = draw_list<THREADS>(sh, count, A.uniforms[r], f.max, s.c);
-      else if (!general) token = draw_tiles<LT, THREADS>(row, V, sh, A.uniforms[r], f.max, s.c);
+      else if (count > 0)
+        token = draw_entries<THREADS, kCand / THREADS, true>(
+            count, A.uniforms[r], sh.bucket, sh.red, [&](int i, int& id, double& mass) {
+              const unsigned long long x = sh.list[i];
+              const float z = key_logit(~(uint32_t)(x >> 32));
+              id = (int)(uint32_t)x;
+              mass = row_keeps(f, z, id) ? weight(z, f.max, f.scale, sh.table) : 0.0;
+            });
       else
-        token = block_draw<THREADS>(V, A.uniforms[r], *reinterpret_cast<DrawShared*>(lds),
-                                    [&](int e) {
-                                      const float z = clean_logit(logit_at(row, e));
-                                      return row_keeps(f, z, e) ? weight(z, f.max, f.scale) : 0.0;
-                                    });
+        token = draw_tiles<LT, THREADS>(row, V, sh, A.uniforms[r], f.max, s.c);
     }
     if (threadIdx.x == 0) A.out_tokens[r] = token;
   }
@@ -962,9 +1089,55 @@ __global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
       __syncthreads();                              // the kept tokens' own values after the zeros
       for (int i = threadIdx.x; i < count; i += THREADS) {
         const unsigned long long x = sh.list[i];
-        q[x >> 32] = (float)(weight(key_logit((uint32_t)x), f.max, f.scale) * f.inv_sum);
+        const float z = key_logit(~(uint32_t)(x >> 32));
+        if (row_keeps(f, z, (uint32_t)x))
+          q[(uint32_t)x] = (float)(weight(z, f.max, f.scale, sh.table) * f.inv_sum);
       }
     } else {
+      for (int e = threadIdx.x; e < V; e += THREADS)
+        __builtin_nontemporal_store(
+            (float)(weight(clean_logit(logit_at(row, e)), f.max, f.scale, sh.table) * f.inv_sum), q + e);
+    }
+  }
+}
+
+// The rows that filter_rows_kernel left (their counts say so): every filter by
+// a radix search over the whole row, one workgroup per row in turn.
+constexpr int kGeneralThreads = 1024;
+template <typename LT>
+__global__ __launch_bounds__(kGeneralThreads) void filter_general_kernel(FilterLaunch A) {
+  constexpr int THREADS = kGeneralThreads;
+  __shared__ union {
+    FilterShared<THREADS> filter;
+    DrawShared draw;
+  } sh;
+  const int V = A.V;
+  const long rows = (long)A.B * A.per_seq;
+  for (long r = blockIdx.x; r < rows; r += gridDim.x) {
+    if (A.list_counts[r] != kGeneralRow) continue;
+    int errors = 0;
+    const FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps,
+                                             A.min_ps, (int)(r / A.per_seq), V, errors);
+    const LT* row = static_cast<const LT*>(A.logits) +
+                    (A.row_index ? (long)A.row_index[r] : r) * A.row_stride;
+    __syncthreads();                                // the last row's draw, and every read of its count
+    const sv_filter_row f = filter_row<LT, THREADS>(row, V, s, sh.filter);
+    if (f.n_kept == 0) errors |= SV_DEVERR_EMPTY_ROW;
+    if (threadIdx.x == 0) {
+      if (errors) flag_error(A.device_error, errors);
+      if (A.out_rows) A.out_rows[r] = f;
+      A.list_counts[r] = -1;
+    }
+    if (A.out_tokens) {
+      // an empty row has no mass: token 0
+      const int token = f.n_kept == 0 ? 0 : block_draw<THREADS>(V, A.uniforms[r], sh.draw, [&](int e) {
+        const float z = clean_logit(logit_at(row, e));
+        return row_keeps(f, z, e) ? weight(z, f.max, f.scale) : 0.0;
+      });
+      if (threadIdx.x == 0) A.out_tokens[r] = token;
+    }
+    if (A.out_probs) {
+      float* q = A.out_probs + r * V;
       for (int e = threadIdx.x; e < V; e += THREADS)
         __builtin_nontemporal_store((float)row_prob(f, logit_at(row, e), e), q + e);
     }
@@ -975,7 +1148,7 @@ template <typename LT, bool QL>
 __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(FilteredVerifyLaunch A) {
   __shared__ DrawShared draw;
   __shared__ double red[kVerifyThreads / kWave];
-  __shared__ int redi[kVerifyThreads / kWave];
+  __shared__ unsigned long long bucket[256];
   __shared__ int sh_a;
   const int b = blockIdx.x, K = A.K, V = A.V;
   const int l = lane_id();
@@ -1041,44 +1214,24 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
     const int count = A.list_counts[row0 + a];
     token = -1;
     if (count >= 0) {
-      // the kept tokens alone, in vocabulary order
+      // the kept tokens alone
       const int32_t* list = A.lists + (row0 + a) * kCand;
       const long dr = a < K ? drafter_row(a) : -1;
       sv_filter_row fq{};
       if constexpr (QL) { if (a < K) fq = A.ddesc[(long)b * K + a]; }
-      const int chunk = (count + kVerifyThreads - 1) / kVerifyThreads;
-      const int r0 = min((int)threadIdx.x * chunk, count), r1 = min(r0 + chunk, count);
-      double r[kCand / kVerifyThreads], p[kCand / kVerifyThreads], rs = 0.0, ps = 0.0, total;
-#pragma unroll
-      for (int i = 0; i < kCand / kVerifyThreads; ++i) {
-        r[i] = p[i] = 0.0;
-        if (r0 + i < r1) {
-          const int e = list[r0 + i];
-          p[i] = row_prob(f, logit_at(za, e), e);
-          r[i] = a < K ? fmax(0.0, p[i] - q_at(a, dr, fq, e)) : p[i];
-        }
-        rs += r[i];
-        ps += p[i];
-      }
-      double run = block_scan<kVerifyThreads>(rs, red, total);
-      if (!(total > 0.0)) {                          // q covers p: draw from p
-        run = block_scan<kVerifyThreads>(ps, red, total);
-#pragma unroll
-        for (int i = 0; i < kCand / kVerifyThreads; ++i) r[i] = p[i];
-      }
-      const double target = (double)u * total;
-      int first = INT32_MAX, any = -1;
-#pragma unroll
-      for (int i = 0; i < kCand / kVerifyThreads; ++i) {
-        run += r[i];
-        if (r[i] > 0.0) {
-          any = r0 + i;
-          if (run > target) first = min(first, r0 + i);
-        }
-      }
-      first = block_reduce<kVerifyThreads>(first, redi, OpMin());
-      any = block_reduce<kVerifyThreads>(any, redi, OpMax());
-      token = list[first == INT32_MAX ? any : first];
+      if (a < K)
+        token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
+            count, u, bucket, red, [&](int i, int& id, double& mass) {
+              id = list[i];
+              const double p = row_prob(f, logit_at(za, id), id);
+              mass = p > 0.0 ? fmax(0.0, p - q_at(a, dr, fq, id)) : 0.0;
+            });
+      if (token < 0)                                 // a = K, or q covers p
+        token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
+            count, u, bucket, red, [&](int i, int& id, double& mass) {
+              id = list[i];
+              mass = row_prob(f, logit_at(za, id), id);
+            });
     } else if (a < K) {
       const long dr = drafter_row(a);
       sv_filter_row fq{};
@@ -1112,9 +1265,9 @@ struct FilterWorkspace {
       where = at;
       at += (size + 15) / 16 * 16;
     };
+    part(counts, n * sizeof(int32_t));
     if (verify) {
       part(rows, n * sizeof(sv_filter_row));
-      part(counts, n * sizeof(int32_t));
       part(lists, n * kCand * sizeof(int32_t));
     }
     if (streams_apart(n, V)) {
@@ -1130,7 +1283,7 @@ template <typename LT, int THREADS, bool PRE>
 void launch_rows(const FilterLaunch& L, hipStream_t stream) {
   const int tiles = (L.V + kRowTile - 1) / kRowTile;
   const size_t gm = (size_t)tiles * (8 / group_octets(L.V)) * kWave * sizeof(float);
-  const size_t lds = std::max(sizeof(RowShared<THREADS>) + gm, sizeof(FilterShared<THREADS>));
+  const size_t lds = sizeof(RowShared<THREADS>) + gm;
   filter_rows_kernel<LT, THREADS, PRE>
       <<<dim3((unsigned)((long)L.B * L.per_seq)), THREADS, lds, stream>>>(L);
 }
@@ -1155,7 +1308,15 @@ hipError_t launch_filter(const FilterLaunch& L, hipStream_t stream) {
     launch_rows<LT, 256, false>(L, stream);
     trace_after(stream, SV_KERNEL_FILTER_ROWS);
   }
-  return hipGetLastError();
+  hipError_t e = hipGetLastError();
+  // every token of a short row fits the list
+  if (e == hipSuccess && L.V > kCand) {
+    trace_before(stream, SV_KERNEL_FILTER_ROWS);
+    filter_general_kernel<LT><<<dim3((unsigned)std::min(rows, 256L)), kGeneralThreads, 0, stream>>>(L);
+    trace_after(stream, SV_KERNEL_FILTER_ROWS);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
@@ -1170,9 +1331,9 @@ hipError_t launch_filter_rows(const FilterLaunch& L0, hipStream_t stream) {
   const FilterWorkspace at((long)L.B * L.per_seq, L.V, L.verify);
   if (L.verify) {
     L.out_rows = reinterpret_cast<sv_filter_row*>(ws + at.rows);
-    L.list_counts = reinterpret_cast<int32_t*>(ws + at.counts);
     L.lists = reinterpret_cast<int32_t*>(ws + at.lists);
   }
+  L.list_counts = reinterpret_cast<int32_t*>(ws + at.counts);
   L.group_max = reinterpret_cast<float*>(ws + at.group_max);
   L.tile_max = reinterpret_cast<float*>(ws + at.tile_max);
   L.tile_sum = reinterpret_cast<double*>(ws + at.tile_sum);

@@ -122,8 +122,8 @@ struct FilterLaunch {
   int verify;                    // filter rows and kept tokens go to the workspace, for the verify
   int32_t* device_error;         // may be NULL
   // in the workspace, set by the launch
-  int32_t* lists;                // kept tokens in vocabulary order, or NULL
-  int32_t* list_counts;          // their number per row; -1: no list
+  int32_t* lists;                // kept tokens (and a few more), or NULL
+  int32_t* list_counts;          // their number per row; -1: no list; -2: left to the general path
   float* group_max;
   float* tile_max;
   double* tile_sum;
