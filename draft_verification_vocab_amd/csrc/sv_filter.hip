@@ -953,56 +953,79 @@ __device__ __forceinline__ int draw_entries(int n, float u, unsigned long long* 
   return prefix;
 }
 
-// The token drawn from a row without filters, whose tile masses stream_row
-// left in sh.tile_s.
-template <typename LT, int THREADS>
-__device__ __forceinline__ int draw_tiles(const LT* row, int V, RowShared<THREADS>& sh, float u, float m, double c) {
+// The tile in which the running total of the tiles' masses first exceeds
+// target (the last with mass if rounding leaves none; -1 if none has mass), and
+// the total before it.  Every wave finds the same.
+__device__ __forceinline__ int find_tile(const double* mass, int tiles, float u, double& target,
+                                         double& before) {
+  constexpr int PER = kRowTiles / kWave;
   const int l = lane_id();
-  const int tiles = (V + kRowTile - 1) / kRowTile;
-  __syncthreads();
-  if (threadIdx.x < kWave) {
-    constexpr int PER = kRowTiles / kWave;
-    double x[PER], mine = 0.0;
+  double x[PER], mine = 0.0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      x[i] = l * PER + i < tiles ? sh.tile_s[l * PER + i] : 0.0;
-      mine += x[i];
-    }
-    const double incl = wave_inclusive_scan(mine);
-    const double target = (double)u * __shfl(incl, kWave - 1);
-    double run = incl - mine, before = 0.0;
-    int hit = -1, any = -1;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (x[i] > 0.0) {
-        any = l * PER + i;
-        if (hit < 0 && run + x[i] > target) { hit = l * PER + i; before = run; }
-      }
-      run += x[i];
-    }
-    const unsigned long long hits = __ballot(hit >= 0), anys = __ballot(any >= 0);
-    const int src = hits ? __ffsll((long long)hits) - 1 : 63 - __clzll((long long)anys);
-    const int tile = __shfl(hits ? hit : any, src);
-    double at = __shfl(before, src);
-    int token = -1, lastpos = 0;
-#pragma unroll 1
-    for (int i = 0; i < kRowTile / kWave && token < 0; ++i) {
-      const int e0 = tile * kRowTile + i * kWave, e = e0 + l;
-      const double y = e < V ? weight(clean_logit(logit_at(row, e)), m, c, sh.table) : 0.0;
-      const double in = wave_inclusive_scan(y);
-      const unsigned long long pos = __ballot(y > 0.0);
-      if (pos) lastpos = e0 + 63 - __clzll((long long)pos);
-      const unsigned long long over = __ballot(y > 0.0 && at + in > target);
-      if (hits && over) token = e0 + __ffsll((long long)over) - 1;
-      at += __shfl(in, kWave - 1);
-    }
-    if (l == 0) sh.token = token < 0 ? lastpos : token;
+  for (int i = 0; i < PER; ++i) {
+    x[i] = l * PER + i < tiles ? mass[l * PER + i] : 0.0;
+    mine += x[i];
   }
-  __syncthreads();
-  return sh.token;
+  const double incl = wave_inclusive_scan(mine);
+  target = (double)u * __shfl(incl, kWave - 1);
+  double run = incl - mine, at = 0.0;
+  int hit = -1, any = -1;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (x[i] > 0.0) {
+      any = l * PER + i;
+      if (hit < 0 && run + x[i] > target) { hit = l * PER + i; at = run; }
+    }
+    run += x[i];
+  }
+  const unsigned long long hits = __ballot(hit >= 0), anys = __ballot(any >= 0);
+  if (!anys) return -1;
+  const int src = hits ? __ffsll((long long)hits) - 1 : 63 - __clzll((long long)anys);
+  before = __shfl(at, src);
+  if (!hits) target = INFINITY;                     // its last token with mass
+  return __shfl(hits ? hit : any, src);
 }
 
-// ---------------------------------------------------------------- kernels
+// The token of tile t at which the running total, `before` ahead of the tile,
+// exceeds target; the tile's last with mass if none does.
+template <int THREADS, typename F>
+__device__ __forceinline__ int find_in_tile(int t, int V, double before, double target, double* red,
+                                            int* redi, F mass) {
+  constexpr int PER = kRowTile / THREADS;
+  const int e0 = t * kRowTile + threadIdx.x * PER;
+  double x[PER], part = 0.0, total;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    x[j] = e0 + j < V ? mass(e0 + j) : 0.0;
+    part += x[j];
+  }
+  double run = before + block_scan<THREADS>(part, red, total);
+  int first = INT32_MAX, any = -1;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    run += x[j];
+    if (x[j] > 0.0) {
+      any = e0 + j;
+      if (run > target) first = min(first, e0 + j);
+    }
+  }
+  first = block_reduce<THREADS>(first, redi, OpMin());
+  any = block_reduce<THREADS>(any, redi, OpMax());
+  return first == INT32_MAX ? any : first;
+}
+
+// The token drawn from a row without filters, whose tile masses are in
+// sh.tile_s.
+template <typename LT, int THREADS>
+__device__ __forceinline__ int draw_tiles(const LT* row, int V, RowShared<THREADS>& sh, float u,
+                                          float m, double c) {
+  double target, before = 0.0;
+  const int t = find_tile(sh.tile_s, (V + kRowTile - 1) / kRowTile, u, target, before);
+  return find_in_tile<THREADS>(t, V, before, target, sh.red, sh.redi, [&](int e) {
+    return weight(clean_logit(logit_at(row, e)), m, c, sh.table);
+  });
+}
+
 // The stream of few rows by all CUs: one wave per tile.
 constexpr int kStreamThreads = 256;
 template <typename LT>
@@ -1049,6 +1072,7 @@ __global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
   sv_filter_row f{0.0, 0.0, -INFINITY, INFINITY, -1, 0};
   const LT* row = static_cast<const LT*>(A.logits) + (there ? ri : 0) * A.row_stride;
   fill_exp_table(sh.table, threadIdx.x, THREADS);
+  if (A.pending && r == 0 && threadIdx.x == 0) *A.pending = 0;
   __syncthreads();
   int count = 0;                                    // entries in sh.list; -1: no list
   if (there && !filter_row_list<LT, THREADS, PRE>(A, r, row, V, s, gm, sh, f, count)) {
@@ -1144,9 +1168,35 @@ __global__ __launch_bounds__(kGeneralThreads) void filter_general_kernel(FilterL
   }
 }
 
+// q of the drafts of one sequence, dense or from the drafter's logits.
+template <typename LT, bool QL>
+struct DrafterQ {
+  const float* probs;                // draft k's row of dense q
+  const LT* logits;                  // its drafter row, NULL if there is none (q = 0)
+  sv_filter_row row;
+  bool missing;
+  __device__ __forceinline__ DrafterQ(const FilteredVerifyLaunch& A, int b, int k) {
+    const long i = (long)b * A.K + k;
+    missing = false;
+    if constexpr (QL) {
+      const long dr = A.drows ? (long)A.drows[i] : i;
+      missing = dr < 0 || dr >= A.d_rows;
+      logits = missing ? nullptr : static_cast<const LT*>(A.dlogits) + dr * A.d_stride;
+      row = A.ddesc[i];
+    } else {
+      probs = A.draft_probs + i * A.V;
+    }
+  }
+  __device__ __forceinline__ double at(int x) const {
+    if constexpr (QL) return logits ? row_prob(row, logit_at(logits, x), x) : 0.0;
+    else return (double)probs[x];
+  }
+};
+
+// The accept scan and, where the row of the first rejection has a list, the new
+// token; other sequences are left to residual_kernel.
 template <typename LT, bool QL>
 __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(FilteredVerifyLaunch A) {
-  __shared__ DrawShared draw;
   __shared__ double red[kVerifyThreads / kWave];
   __shared__ unsigned long long bucket[256];
   __shared__ int sh_a;
@@ -1154,39 +1204,21 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
   const int l = lane_id();
   const long row0 = (long)b * (K + 1);
   const LT* z0 = static_cast<const LT*>(A.logits) + row0 * A.row_stride;
-  // q of draft k at token x
-  const auto q_at = [&](int k, long dr, const sv_filter_row& f, int x) -> double {
-    if constexpr (QL) {
-      if (dr < 0) return 0.0;
-      return row_prob(f, logit_at(static_cast<const LT*>(A.dlogits) + dr * A.d_stride, x), x);
-    } else {
-      return (double)A.draft_probs[((long)b * K + k) * V + x];
-    }
-  };
-  const auto drafter_row = [&](int k) -> long {
-    if constexpr (!QL) return 0;
-    const long i = (long)b * K + k;
-    const long dr = A.drows ? (long)A.drows[i] : i;
-    return dr >= 0 && dr < A.d_rows ? dr : -1;
-  };
   int errors = 0;
   if (threadIdx.x < kWave) {
     bool accepted = false;
     if (l < K) {
       const sv_filter_row f = A.rows[row0 + l];
-      const bool greedy = f.scale == 0.0;
       const int x = A.draft_tokens[(long)b * K + l];
       double p = 0.0;
       if (x >= 0 && x < V) {
         p = row_prob(f, logit_at(z0 + l * A.row_stride, x), x);
-        if (greedy) {
+        if (f.scale == 0.0) {                        // greedy
           accepted = x == f.last;
         } else if (p > 0.0) {
-          const long dr = drafter_row(l);
-          if (dr < 0) errors |= SV_DEVERR_ROW_INDEX;
-          sv_filter_row fq{};
-          if constexpr (QL) fq = A.ddesc[(long)b * K + l];
-          accepted = (double)A.uniforms[row0 + l] * q_at(l, dr, fq, x) < p;
+          const DrafterQ<LT, QL> q(A, b, l);
+          if (q.missing) errors |= SV_DEVERR_ROW_INDEX;
+          accepted = (double)A.uniforms[row0 + l] * q.at(x) < p;
         }
       } else {
         errors |= SV_DEVERR_DRAFT_TOKEN;
@@ -1204,48 +1236,134 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
   const int a = sh_a;
   const sv_filter_row f = A.rows[row0 + a];
   const LT* za = z0 + (long)a * A.row_stride;
-  int token = 0;
-  if (f.n_kept == 0) {
-    token = 0;
-  } else if (f.scale == 0.0) {
+  int token = 0;                                     // of an empty row
+  if (f.n_kept > 0 && f.scale == 0.0) {
     token = f.last;
-  } else {
+  } else if (f.n_kept > 0) {
     const float u = A.uniforms[row0 + K];
     const int count = A.list_counts[row0 + a];
-    token = -1;
-    if (count >= 0) {
-      // the kept tokens alone
-      const int32_t* list = A.lists + (row0 + a) * kCand;
-      const long dr = a < K ? drafter_row(a) : -1;
-      sv_filter_row fq{};
-      if constexpr (QL) { if (a < K) fq = A.ddesc[(long)b * K + a]; }
-      if (a < K)
-        token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
-            count, u, bucket, red, [&](int i, int& id, double& mass) {
-              id = list[i];
-              const double p = row_prob(f, logit_at(za, id), id);
-              mass = p > 0.0 ? fmax(0.0, p - q_at(a, dr, fq, id)) : 0.0;
-            });
-      if (token < 0)                                 // a = K, or q covers p
-        token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
-            count, u, bucket, red, [&](int i, int& id, double& mass) {
-              id = list[i];
-              mass = row_prob(f, logit_at(za, id), id);
-            });
-    } else if (a < K) {
-      const long dr = drafter_row(a);
-      sv_filter_row fq{};
-      if constexpr (QL) fq = A.ddesc[(long)b * K + a];
-      token = block_draw<kVerifyThreads>(V, u, draw, [&](int e) {
-        const double p = row_prob(f, logit_at(za, e), e);
-        return p > 0.0 ? fmax(0.0, p - q_at(a, dr, fq, e)) : 0.0;
-      });
+    if (count < 0) {
+      if (threadIdx.x == 0) {
+        A.done[b] = 0;
+        A.pending[1 + atomicAdd(A.pending, 1)] = b;
+      }
+      return;
     }
-    if (token < 0)
-      token = block_draw<kVerifyThreads>(V, u, draw,
-                                         [&](int e) { return row_prob(f, logit_at(za, e), e); });
+    const int32_t* list = A.lists + (row0 + a) * kCand;
+    token = -1;
+    if (a < K) {
+      const DrafterQ<LT, QL> q(A, b, a);
+      token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
+          count, u, bucket, red, [&](int i, int& id, double& mass) {
+            id = list[i];
+            const double p = row_prob(f, logit_at(za, id), id);
+            mass = p > 0.0 ? fmax(0.0, p - q.at(id)) : 0.0;
+          });
+    }
+    if (token < 0)                                   // a = K, or q covers p
+      token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
+          count, u, bucket, red, [&](int i, int& id, double& mass) {
+            id = list[i];
+            mass = row_prob(f, logit_at(za, id), id);
+          });
   }
   if (threadIdx.x == 0) A.out_tokens[row0 + a] = token;
+}
+
+// The new tokens of the sequences whose row a has no list (no filter, or a
+// nucleus of thousands): the residual's and p's mass of every tile of the row,
+// one wave per tile over all CUs; the workgroup that finishes a sequence's last
+// tiles finds the token.
+template <typename LT, bool QL>
+__global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerifyLaunch A) {
+  constexpr int WAVES = kVerifyThreads / kWave;
+  __shared__ double table[kExpTable];
+  __shared__ double red[WAVES];
+  __shared__ int redi[WAVES];
+  __shared__ double mass[kRowTiles];
+  __shared__ int sh_last;
+  const int pending = A.pending[0];
+  const int K = A.K, V = A.V;
+  const int tiles = (V + kRowTile - 1) / kRowTile, parts = (tiles + WAVES - 1) / WAVES;
+  if ((long)blockIdx.x >= (long)pending * parts) return;
+  fill_exp_table(table, threadIdx.x, kVerifyThreads);
+  __syncthreads();
+  const int w = threadIdx.x / kWave, l = lane_id();
+  for (long item = blockIdx.x; item < (long)pending * parts; item += gridDim.x) {
+    const int b = A.pending[1 + item / parts];
+    const long row0 = (long)b * (K + 1);
+    const int a = A.out_num_accepted[b];
+    const sv_filter_row f = A.rows[row0 + a];
+    const LT* za = static_cast<const LT*>(A.logits) + (row0 + a) * A.row_stride;
+    const bool residual = a < K;
+    const DrafterQ<LT, QL> q(A, b, residual ? a : 0);
+    double* rmass = A.tile_mass + (long)b * 2 * tiles;
+    double* pmass = rmass + tiles;
+    const auto p_at = [&](float z, int x) {
+      z = clean_logit(z);
+      return row_keeps(f, z, x) ? weight(z, f.max, f.scale, table) * f.inv_sum : 0.0;
+    };
+    const auto q_at = [&](int x) {
+      if constexpr (QL) {
+        if (!q.logits) return 0.0;
+        const float z = clean_logit(logit_at(q.logits, x));
+        return row_keeps(q.row, z, x) ? weight(z, q.row.max, q.row.scale, table) * q.row.inv_sum
+                                      : 0.0;
+      } else {
+        return (double)q.probs[x];
+      }
+    };
+    const auto r_at = [&](int x) {
+      const double p = p_at(logit_at(za, x), x);
+      return p > 0.0 ? fmax(0.0, p - q_at(x)) : 0.0;
+    };
+    const int t = (int)(item % parts) * WAVES + w;
+    if (t < tiles) {
+      double rs = 0.0, ps = 0.0;
+#pragma unroll 4
+      for (int i = 0; i < kRowTile / kWave; ++i) {
+        const int x = t * kRowTile + i * kWave + l;
+        if (x < V) {
+          const double p = p_at(logit_at(za, x), x);
+          ps += p;
+          if (residual && p > 0.0) rs += fmax(0.0, p - q_at(x));
+        }
+      }
+      rs = wave_sum(rs);
+      ps = wave_sum(ps);
+      if (l == 0) {
+        st_coherent(rmass + t, rs);
+        st_coherent(pmass + t, ps);
+      }
+      wait_stores_performed();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh_last = atomicAdd(&A.done[b], 1) == parts - 1;
+    __syncthreads();
+    if (sh_last) {                                   // uniform
+      const float u = A.uniforms[row0 + K];
+      double target, before = 0.0;
+      int tile = -1;
+      if (residual) {
+        for (int i = threadIdx.x; i < tiles; i += kVerifyThreads) mass[i] = ld_coherent(rmass + i);
+        __syncthreads();
+        tile = find_tile(mass, tiles, u, target, before);
+      }
+      int token;
+      if (tile >= 0) {
+        token = find_in_tile<kVerifyThreads>(tile, V, before, target, red, redi, r_at);
+      } else {                                       // a = K, or q covers p
+        __syncthreads();
+        for (int i = threadIdx.x; i < tiles; i += kVerifyThreads) mass[i] = ld_coherent(pmass + i);
+        __syncthreads();
+        tile = find_tile(mass, tiles, u, target, before);
+        token = find_in_tile<kVerifyThreads>(tile, V, before, target, red, redi,
+                                             [&](int x) { return p_at(logit_at(za, x), x); });
+      }
+      if (threadIdx.x == 0) A.out_tokens[row0 + a] = token;
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace
@@ -1257,7 +1375,8 @@ bool streams_apart(long rows, int V) { return V > kCand && rows <= 512; }
 
 // The parts of the workspace, in order; each starts at a multiple of 16 bytes.
 struct FilterWorkspace {
-  size_t rows = 0, counts = 0, lists = 0, group_max = 0, tile_max = 0, tile_sum = 0, bytes = 0;
+  size_t rows = 0, counts = 0, lists = 0, pending = 0, done = 0, tile_mass = 0;
+  size_t group_max = 0, tile_max = 0, tile_sum = 0, bytes = 0;
   FilterWorkspace(long n, int V, bool verify) {
     const size_t tiles = (V + kRowTile - 1) / kRowTile;
     size_t at = 0;
@@ -1269,6 +1388,10 @@ struct FilterWorkspace {
     if (verify) {
       part(rows, n * sizeof(sv_filter_row));
       part(lists, n * kCand * sizeof(int32_t));
+      // no more sequences than rows
+      part(pending, (n + 1) * sizeof(int32_t));
+      part(done, n * sizeof(int32_t));
+      part(tile_mass, n * 2 * tiles * sizeof(double));
     }
     if (streams_apart(n, V)) {
       part(group_max, n * tiles * (8 / group_octets(V)) * kWave * sizeof(float));
@@ -1319,6 +1442,24 @@ hipError_t launch_filter(const FilterLaunch& L, hipStream_t stream) {
   return e;
 }
 
+template <typename LT, bool QL>
+hipError_t launch_verify_tail(const FilteredVerifyLaunch& L, hipStream_t stream) {
+  trace_before(stream, SV_KERNEL_FILTERED_VERIFY);
+  filtered_verify_kernel<LT, QL><<<dim3((unsigned)L.B), kVerifyThreads, 0, stream>>>(L);
+  trace_after(stream, SV_KERNEL_FILTERED_VERIFY);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && L.V > kCand) {              // a shorter row always has a list
+    const int waves = kVerifyThreads / kWave;
+    const long parts = ((L.V + kRowTile - 1) / kRowTile + waves - 1) / waves;
+    trace_before(stream, SV_KERNEL_FILTERED_VERIFY);
+    residual_kernel<LT, QL><<<dim3((unsigned)std::min(L.B * parts, 2048L)), kVerifyThreads, 0,
+                              stream>>>(L);
+    trace_after(stream, SV_KERNEL_FILTERED_VERIFY);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
 }  // namespace
 
 size_t filter_workspace_bytes(long n_rows, int V) {
@@ -1332,6 +1473,7 @@ hipError_t launch_filter_rows(const FilterLaunch& L0, hipStream_t stream) {
   if (L.verify) {
     L.out_rows = reinterpret_cast<sv_filter_row*>(ws + at.rows);
     L.lists = reinterpret_cast<int32_t*>(ws + at.lists);
+    L.pending = reinterpret_cast<int32_t*>(ws + at.pending);
   }
   L.list_counts = reinterpret_cast<int32_t*>(ws + at.counts);
   L.group_max = reinterpret_cast<float*>(ws + at.group_max);
@@ -1347,6 +1489,9 @@ hipError_t launch_filtered_verify(const FilteredVerifyLaunch& L0, hipStream_t st
   L.rows = reinterpret_cast<sv_filter_row*>(ws + at.rows);
   L.list_counts = reinterpret_cast<int32_t*>(ws + at.counts);
   L.lists = reinterpret_cast<int32_t*>(ws + at.lists);
+  L.pending = reinterpret_cast<int32_t*>(ws + at.pending);
+  L.done = reinterpret_cast<int32_t*>(ws + at.done);
+  L.tile_mass = reinterpret_cast<double*>(ws + at.tile_mass);
   FilterLaunch F{};
   F.logits = L.logits;
   F.row_stride = L.row_stride;
@@ -1365,17 +1510,10 @@ hipError_t launch_filtered_verify(const FilteredVerifyLaunch& L0, hipStream_t st
   F.device_error = L.device_error;
   hipError_t e = launch_filter_rows(F, stream);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)L.B);
-  trace_before(stream, SV_KERNEL_FILTERED_VERIFY);
-  if (L.bf16) {
-    if (L.lq) filtered_verify_kernel<uint16_t, true><<<grid, kVerifyThreads, 0, stream>>>(L);
-    else filtered_verify_kernel<uint16_t, false><<<grid, kVerifyThreads, 0, stream>>>(L);
-  } else {
-    if (L.lq) filtered_verify_kernel<float, true><<<grid, kVerifyThreads, 0, stream>>>(L);
-    else filtered_verify_kernel<float, false><<<grid, kVerifyThreads, 0, stream>>>(L);
-  }
-  trace_after(stream, SV_KERNEL_FILTERED_VERIFY);
-  return hipGetLastError();
+  return L.bf16 ? (L.lq ? launch_verify_tail<uint16_t, true>(L, stream)
+                        : launch_verify_tail<uint16_t, false>(L, stream))
+                : (L.lq ? launch_verify_tail<float, true>(L, stream)
+                        : launch_verify_tail<float, false>(L, stream));
 }
 
 }  // namespace sv

@@ -124,6 +124,7 @@ struct FilterLaunch {
   // in the workspace, set by the launch
   int32_t* lists;                // kept tokens (and a few more), or NULL
   int32_t* list_counts;          // their number per row; -1: no list; -2: left to the general path
+  int32_t* pending;              // its counter is cleared here for the verify; or NULL
   float* group_max;
   float* tile_max;
   double* tile_sum;
@@ -155,6 +156,9 @@ struct FilteredVerifyLaunch {
   sv_filter_row* rows;           // [B*(K+1)]
   int32_t* list_counts;
   int32_t* lists;
+  int32_t* pending;              // number of sequences left to residual_kernel, then those
+  int32_t* done;                 // [B] workgroups that have finished a part of theirs
+  double* tile_mass;             // [B][2][tiles]
 };
 
 struct AppendLaunch {
