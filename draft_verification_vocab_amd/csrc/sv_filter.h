@@ -68,9 +68,26 @@ __device__ __forceinline__ double exp2_f64(double x) {
 // scaling are of the slower kind (for the long sums); with the exponential
 // series up to r^3 (LONG) to 1e-14.
 constexpr int kExpTable = 512;
+struct ExpTable {
+  double v[kExpTable];
+  constexpr ExpTable() : v() {
+    for (int i = 0; i < kExpTable; ++i) {
+      // 2^(i/512) as the square of the exponential series of half its logarithm
+      const double y = 0.69314718055994530942 * i / (2.0 * kExpTable);
+      double term = 1.0, sum = 0.0;
+      for (int k = 24; k >= 0; --k) {               // smallest terms first
+        term = 1.0;
+        for (int j = 1; j <= k; ++j) term *= y / j;
+        sum += term;
+      }
+      v[i] = sum * sum;
+    }
+  }
+};
+__device__ constexpr ExpTable kExp2Table;
 __device__ __forceinline__ void fill_exp_table(double* table, int t, int threads) {
-#pragma unroll 1
-  for (int i = t; i < kExpTable; i += threads) table[i] = exp2_f64(i * (1.0 / kExpTable));
+#pragma unroll 2
+  for (int i = t; i < kExpTable; i += threads) table[i] = kExp2Table.v[i];
 }
 template <bool LONG>
 __device__ __forceinline__ double exp2_table(double x, const double* table) {
@@ -146,6 +163,18 @@ __device__ __forceinline__ FilterSettings filter_settings(const float* temperatu
 }
 
 // ---------------------------------------------------------------- workgroup reductions
+// A value that all lanes hold, in scalar registers.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one or two registers");
+  int w[sizeof(T) / 4];
+  __builtin_memcpy(w, &x, sizeof(T));
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) / 4; ++i) w[i] = __builtin_amdgcn_readfirstlane(w[i]);
+  __builtin_memcpy(&x, w, sizeof(T));
+  return x;
+}
+
 // Each gives every thread the result; sm holds one entry per wave.
 template <int THREADS, typename T, typename OP>
 __device__ __forceinline__ T block_reduce(T x, T* sm, OP op) {
@@ -157,7 +186,7 @@ __device__ __forceinline__ T block_reduce(T x, T* sm, OP op) {
   x = sm[0];
 #pragma unroll
   for (int i = 1; i < THREADS / kWave; ++i) x = op(x, sm[i]);
-  return x;
+  return uniform(x);
 }
 struct OpAdd { template <typename T> __device__ T operator()(T a, T b) const { return a + b; } };
 struct OpMax { template <typename T> __device__ T operator()(T a, T b) const { return a > b ? a : b; } };

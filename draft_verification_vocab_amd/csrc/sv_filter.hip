@@ -343,7 +343,7 @@ constexpr int kTopBins = 256;          // histogram of the group maxima
 constexpr int kFirst = 96;             // groups whose tokens a nucleus row looks at first
 constexpr int kGeneralRow = -2;        // list_counts: the row takes the general path
 constexpr int kMaxListK = 1024;        // largest top-k taken through the candidate list
-constexpr int kRankN = 512;            // most entries sorted by counting
+constexpr int kWaveList = 128;         // most candidates that one wave cuts and draws from
 
 // Octets per group: 8, or fewer as long as there are at most 3200 groups.
 __host__ __device__ __forceinline__ int group_octets(int V) {
@@ -358,6 +358,7 @@ struct RowShared {
     struct { uint32_t cnt[kTopBins], mass[kTopBins]; } top;
     uint16_t queue[kQueue];
     unsigned long long bucket[256];
+    struct { unsigned long long entry[kWaveList]; double w[kWaveList]; int id[kWaveList]; } sorted;
   };
   double tile_s[kRowTiles];
   float tile_m[kRowTiles];
@@ -366,50 +367,11 @@ struct RowShared {
   int redi[THREADS / kWave];
   int n, nq, token, bin, above;
   float frac;
+  // what the first wave finds in a short list
+  int found;
+  double got;
+  sv_filter_row row;
 };
-
-// n entries of sh.list in increasing order, in sh.list.  Workgroup-wide.
-template <int THREADS>
-__device__ __forceinline__ void sort_list(RowShared<THREADS>& sh, int n) {
-  __syncthreads();
-  if (n <= kRankN) {
-    // each entry's place is the number of smaller ones (no two are equal)
-    constexpr int PER = (kRankN + THREADS - 1) / THREADS;
-    unsigned long long x[PER];
-    int rank[PER];
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const int i = p * THREADS + threadIdx.x;
-      x[p] = i < n ? sh.list[i] : 0;
-      rank[p] = 0;
-    }
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const unsigned long long y = sh.list[j];
-#pragma unroll
-      for (int p = 0; p < PER; ++p) rank[p] += y < x[p];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int p = 0; p < PER; ++p)
-      if (p * THREADS + (int)threadIdx.x < n) sh.list[rank[p]] = x[p];
-    __syncthreads();
-    return;
-  }
-  int N = 2 * kRankN;
-  while (N < n) N <<= 1;
-  for (int i = n + threadIdx.x; i < N; i += THREADS) sh.list[i] = ~0ull;
-  for (int size = 2; size <= N; size <<= 1)
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < N / 2; i += THREADS) {
-        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
-        const unsigned long long a = sh.list[lo], b = sh.list[hi];
-        if ((a > b) == ((lo & size) == 0)) { sh.list[lo] = b; sh.list[hi] = a; }
-      }
-    }
-  __syncthreads();
-}
 
 // Exclusive running totals over the workgroup's threads, and the total.
 template <int THREADS>
@@ -424,12 +386,11 @@ __device__ __forceinline__ double block_scan(double x, double* sm, double& total
     if (i < (int)threadIdx.x / kWave) off += sm[i];
     all += sm[i];
   }
-  total = all;
+  total = uniform(all);
   return off + (incl - x);
 }
 
-// Entries of the list: in the order, (~key, index); in vocabulary order,
-// (index, key).
+// An entry of the list; their order is that of the tokens.
 __device__ __forceinline__ unsigned long long order_entry(uint32_t key, int e) {
   return ((unsigned long long)~key << 32) | (uint32_t)e;
 }
@@ -591,10 +552,15 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
   const bool by_mass = k == 0;
   if (hi < lo) return kKeyNegInf + 1;
   float mass = 0.f;                    // estimated mass found
+  // by count, a binade below the maximum first: the threshold of a row's largest
+  // logits is mostly there, in narrow bins
+  const uint32_t floor = lo;
+  bool near = !by_mass && hi - lo > 0x800000u;
+  if (near) lo = hi - 0x800000u;
 #pragma unroll 1
-  for (int level = 0; level < 4; ++level) {
-    int shift = 0;
-    while (((hi - lo) >> shift) >= (uint32_t)kTopBins) ++shift;
+  for (int level = 0; level < 5; ++level) {
+    // hi - lo < 256 << shift
+    const int shift = max(0, 24 - __clz((int)(hi - lo | 1u)));
     __syncthreads();
     for (int i = threadIdx.x; i < kTopBins; i += THREADS) sh.top.cnt[i] = sh.top.mass[i] = 0;
     if (threadIdx.x == 0) sh.bin = -1;
@@ -672,13 +638,21 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
       }
     }
     __syncthreads();
-    const int b = sh.bin;
-    // not reached: every token, or (by mass, inside a bin that seemed to reach
-    // it) what there is
-    if (b < 0) return level == 0 ? kKeyNegInf + 1 : lo;
-    above = sh.above;
-    mass = sh.frac;
-    const int in = (int)sh.top.cnt[b];
+    const int b = uniform(sh.bin);
+    if (b < 0) {
+      if (near) {                                   // not within the binade
+        near = false;
+        lo = floor;
+        continue;
+      }
+      // not reached: every token, or (by mass, inside a bin that seemed to
+      // reach it) what there is
+      return lo == floor ? kKeyNegInf + 1 : lo;
+    }
+    near = false;
+    above = uniform(sh.above);
+    mass = uniform(sh.frac);
+    const int in = (int)uniform(sh.top.cnt[b]);
     const uint32_t top = hi - ((uint32_t)b << shift);
     const uint32_t width = (1u << shift) - 1;
     const uint32_t bottom = top - lo > width ? top - width : lo;
@@ -706,41 +680,351 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
       if (q < kQueue) sh.queue[q] = (uint16_t)i;
     }
   __syncthreads();
-  const int nq = sh.nq;
+  const int nq = uniform(sh.nq);
   if (nq > kQueue) return -1;
+  // four octets a thread at a time, to have their loads in flight together
+  const int items = nq * G;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < nq * G; i += THREADS) {
-    const int q = sh.queue[i / G], u = q / kWave % per * G + i % G;
-    const int e = q / (per * kWave) * kRowTile + u * kTile + q % kWave * 8;
-    float z[8];
-    if (e + 8 <= V) {
-      load8(row + e, z);
-    } else {
+  for (int i0 = threadIdx.x; i0 < items; i0 += 4 * THREADS) {
+    Raw<LT> raw[4];
+    int e[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = e + j < V ? logit_at(row, e + j) : -INFINITY;
+    for (int p = 0; p < 4; ++p) {
+      const int i = min(i0 + p * THREADS, items - 1);
+      const int q = sh.queue[i / G], u = q / kWave % per * G + i % G;
+      e[p] = q / (per * kWave) * kRowTile + u * kTile + q % kWave * 8;
+      if (e[p] + 8 <= V) raw8(row + e[p], raw[p]);
+      else raw8_end(row, e[p], V, raw[p]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = clean_logit(z[j]);
-      if (x >= zt) {
-        const int at = atomicAdd(&sh.n, 1);
-        if (at < kCand) sh.list[at] = order_entry(logit_key(x), e + j);
+    for (int p = 0; p < 4; ++p) {
+      if (i0 + p * THREADS >= items) break;
+      float z[8];
+      unpack(raw[p], z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = clean_logit(z[j]);
+        if (x >= zt) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kCand) sh.list[at] = order_entry(logit_key(x), e[p] + j);
+        }
       }
     }
   }
   __syncthreads();
-  return sh.n > kCand ? -1 : sh.n;
+  const int n = uniform(sh.n);
+  return n > kCand ? -1 : n;
 }
 
-// The kept set of one row through the candidate list.  Returns false where the
-// row has to take the general path (filter_row): more candidates than the list
-// holds, or a large top-k.  The kept tokens are in sh.list[0 .. count), in any
-// order; count is -1 for rows without a list.
+// Search of a running total over n numbers, digit by digit (8 bits, most
+// significant first): the smallest key(i) of BITS bits at which the sum of x(i)
+// over the keys up to it reaches target (STRICT: exceeds it), or the largest key
+// with x > 0 if none does.  x are integers, so the sums do not depend on the
+// order in which LDS adds them.  Also the sums over smaller keys and over that
+// key.  Workgroup-wide; thread t sees the numbers t, t + THREADS, ...
+template <int THREADS, int BITS, bool STRICT, typename K, typename X>
+__device__ __forceinline__ uint32_t digit_search(int n, K key, X x, double target,
+                                                 unsigned long long* bucket,
+                                                 unsigned long long& before,
+                                                 unsigned long long& inside) {
+  uint32_t prefix = 0;
+  before = inside = 0;
+  bool past = false;                                // no crossing: the last key
+#pragma unroll 1
+  for (int rest = BITS; rest > 0;) {
+    const int bits = rest < 8 ? rest : 8;
+    const int shift = rest - bits;
+    for (int i = threadIdx.x; i < 256; i += THREADS) bucket[i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+      const uint32_t d = key(i);
+      if (rest == 32 || d >> rest == prefix) {
+        const unsigned long long v = x(i);
+        if (v) atomicAdd(&bucket[(d >> shift) & ((1u << bits) - 1)], v);
+      }
+    }
+    __syncthreads();
+    // every wave finds the same bucket
+    const int l = lane_id();
+    unsigned long long m[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { m[i] = bucket[l * 4 + i]; mine += m[i]; }
+    unsigned long long run = mine;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const unsigned long long y = __shfl_up(run, off);
+      if (l >= off) run += y;
+    }
+    run += before - mine;
+    int hit = -1, any = -1;
+    unsigned long long at = 0, in = 0, any_at = 0, any_in = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned long long next = run + m[i];
+      if (m[i]) {
+        any = l * 4 + i;
+        any_at = run;
+        any_in = m[i];
+        const bool over = STRICT ? (double)next > target : (double)next >= target;
+        if (hit < 0 && over && !past) { hit = l * 4 + i; at = run; in = m[i]; }
+      }
+      run = next;
+    }
+    const unsigned long long hits = __ballot(hit >= 0), anys = __ballot(any >= 0);
+    past = past || !hits;
+    const int src = hits ? __ffsll((long long)hits) - 1 : anys ? 63 - __clzll((long long)anys) : 0;
+    prefix = prefix << bits | uniform((uint32_t)__shfl(hits ? hit : any, src));
+    before = uniform(__shfl(hits ? at : any_at, src));
+    inside = uniform(__shfl(hits ? in : any_in, src));
+    __syncthreads();
+    rest -= bits;
+  }
+  return prefix;
+}
+
+// What a list's cut came to.
+enum ListCut { CUT_DONE, CUT_SHORT, CUT_AMBIGUOUS };
+
+// Number of equal weights w, the first of which lies `before` into a running
+// total, that start below target: at least 1, at most ties.
+__device__ __forceinline__ int ties_below(double target, double before, double w, int ties) {
+  const double need = w > 0.0 ? ceil((target - before) / w) : (double)ties;
+  return need >= (double)ties ? ties : need < 1.0 ? 1 : (int)need;
+}
+
+// Top-k, top-p and min-p on n candidates in sh.list, and with `draw` the token
+// of uniform u among the kept ones (sh.token).  sum: the row's sum of weights,
+// or negative where the candidates' (after top-k) counts; slack: how far the
+// target may be off; complete: the list holds every kept token.  Also got, the
+// sum of the candidates' weights.
+//
+// Weights are integers in units of 2^-50 here (sums of 2048 of them fit 62
+// bits and are exact whatever their order).
+template <typename LT, int THREADS>
+__device__ __forceinline__ ListCut cut_list(RowShared<THREADS>& sh, int n, const FilterSettings& s,
+                                            int V, float m, double sum, double slack, bool complete,
+                                            bool draw, float u, sv_filter_row& f, double& got) {
+  static_assert(kCand <= 32 * THREADS, "a bit per entry of a thread");
+  constexpr double UNIT = 0x1p50;
+  // bf16 keys differ in their upper halves only
+  constexpr int KEY_BITS = sizeof(LT) == 2 ? 16 : 32;
+  unsigned kept = ~0u;                              // bit i / THREADS: entry i
+  const auto is_kept = [&](int i) { return (kept >> (i / THREADS)) & 1u; };
+  const auto drop = [&](int i) { kept &= ~(1u << (i / THREADS)); };
+  // ~key: increases along the order
+  const auto digits = [&](int i) { return (uint32_t)(sh.list[i] >> (64 - KEY_BITS)); };
+  const auto id = [&](int i) { return (uint32_t)sh.list[i]; };
+  const auto weight_of = [&](int i) {
+    return weight(key_logit(~(uint32_t)(sh.list[i] >> 32)), m, s.c, sh.table);
+  };
+  const auto one = [&](int i) { return (unsigned long long)is_kept(i); };
+  const auto mass = [&](int i) {
+    return is_kept(i) ? (unsigned long long)rint(weight_of(i) * UNIT) : 0ull;
+  };
+  const auto each = [&](auto f) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += THREADS) f(i);
+  };
+  unsigned long long before, inside;
+  // of the kept entries: those before digits d, and of those with digits d the
+  // first `keep` by index
+  const auto cut_at = [&](uint32_t d, int keep, int ties) {
+    uint32_t last = 0xffffffffu;
+    if (keep < ties) {
+      unsigned long long x, y;
+      last = digit_search<THREADS, 19, false>(
+          n, id, [&](int i) { return digits(i) == d ? one(i) : 0ull; }, (double)keep, sh.bucket, x,
+          y);
+    }
+    each([&](int i) {
+      const uint32_t e = digits(i);
+      if (e > d || (e == d && id(i) > last)) drop(i);
+    });
+  };
+  __syncthreads();                                  // the queue is read, the list written
+  if (s.k < n) {
+    const uint32_t d = digit_search<THREADS, KEY_BITS, false>(n, digits, one, (double)s.k,
+                                                               sh.bucket, before, inside);
+    cut_at(d, s.k - (int)before, (int)inside);
+  }
+  const auto total_mass = [&]() {
+    unsigned long long x = 0;
+    each([&](int i) { x += mass(i); });
+    return block_reduce<THREADS>(x, reinterpret_cast<unsigned long long*>(sh.red), OpAdd());
+  };
+  unsigned long long total = total_mass();
+  got = (double)total / UNIT;
+  if (s.p < 1.0) {
+    const double target = s.p * (sum >= 0.0 ? sum : got);
+    if (!complete && got < target + slack) return CUT_SHORT;
+    const uint32_t d = digit_search<THREADS, KEY_BITS, false>(n, digits, mass, target * UNIT,
+                                                               sh.bucket, before, inside);
+    double w = 0.0;                                 // the weight of the tokens with digits d
+    int ties = 0;
+    each([&](int i) {
+      if (is_kept(i) && digits(i) == d) { ++ties; w = weight_of(i); }
+    });
+    ties = block_reduce<THREADS>(ties, sh.redi, OpAdd());
+    w = block_reduce<THREADS>(w, sh.red, OpMax());
+    const double ahead = (double)before / UNIT;
+    const int keep = ties_below(target, ahead, w, ties);
+    if (slack > 0.0 && (target - (ahead + (keep - 1) * w) <= slack ||
+                        ahead + keep * w - target <= slack))
+      return CUT_AMBIGUOUS;
+    cut_at(d, keep, ties);
+  }
+  if (s.mp > 0.0)
+    each([&](int i) { if (weight_of(i) < s.mp) drop(i); });
+  if (s.p < 1.0 || s.mp > 0.0) total = total_mass();
+  // the last kept entry
+  unsigned long long last = 0;
+  int count = 0;
+  each([&](int i) {
+    if (is_kept(i)) { last = max(last, sh.list[i]); ++count; }
+  });
+  last = block_reduce<THREADS>(last, reinterpret_cast<unsigned long long*>(sh.red), OpMax());
+  count = block_reduce<THREADS>(count, sh.redi, OpAdd());
+  f.inv_sum = UNIT / (double)total;
+  f.min_kept = key_logit(~(uint32_t)(last >> 32));
+  f.last = (int)(uint32_t)last;
+  f.n_kept = count;
+  if (draw) {
+    const uint32_t t = digit_search<THREADS, 19, true>(n, id, mass, (double)u * (double)total,
+                                                       sh.bucket, before, inside);
+    if (threadIdx.x == 0) sh.token = (int)t;
+    __syncthreads();
+  }
+  return CUT_DONE;
+}
+
+// The same for a short list by the first wave, two entries a lane, without
+// barriers but the last: entries sorted by counting the smaller ones, running
+// totals by wave scans in fp64.
+template <int THREADS>
+__device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
+                                                  const FilterSettings& s, float m, double sum,
+                                                  double slack, bool complete, bool draw, float u,
+                                                  sv_filter_row& f, double& got) {
+  __syncthreads();                                  // the queue is read, the list written
+  if (threadIdx.x < kWave) {
+    const int l = lane_id();
+    auto& so = sh.sorted;
+    const unsigned long long e0 = l < n ? sh.list[l] : ~0ull;
+    const unsigned long long e1 = l + kWave < n ? sh.list[l + kWave] : ~0ull;
+    int r0 = 0, r1 = 0;
+    if (n <= kWave) {
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) r0 += sh.list[j] < e0;
+    } else {
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const unsigned long long y = sh.list[j];
+        r0 += y < e0;
+        r1 += y < e1;
+      }
+    }
+    if (l < n) so.entry[r0] = e0;
+    if (l + kWave < n) so.entry[r1] = e1;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    // lane l: places 2l and 2l + 1 of the order
+    const int nk = min(n, s.k);
+    unsigned long long e[2];
+    double w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      e[i] = 2 * l + i < n ? so.entry[2 * l + i] : 0;
+      w[i] = 2 * l + i < nk ? weight(key_logit(~(uint32_t)(e[i] >> 32)), m, s.c, sh.table) : 0.0;
+    }
+    const double incl = wave_inclusive_scan(w[0] + w[1]);
+    const double total = __shfl(incl, kWave - 1);
+    const double run0 = incl - (w[0] + w[1]), run1 = run0 + w[0];
+    const double target = s.p * (sum >= 0.0 ? sum : total);
+    ListCut c = CUT_DONE;
+    int keep = 0;
+    if (s.p < 1.0 && !complete && total < target + slack) {
+      c = CUT_SHORT;
+    } else {
+      bool k[2];
+      int most = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const double run = i ? run1 : run0;
+        const bool in = 2 * l + i < nk && w[i] >= s.mp;
+        k[i] = in && (s.p >= 1.0 || run < target - slack);
+        keep += k[i];
+        most += in && (s.p >= 1.0 || run < target + slack);
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) keep += __shfl_xor(keep, off);
+      if (slack > 0.0) {
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) most += __shfl_xor(most, off);
+        if (most != keep) c = CUT_AMBIGUOUS;
+      }
+      if (c == CUT_DONE) {
+        const double part = (k[0] ? w[0] : 0.0) + (k[1] ? w[1] : 0.0);
+        const double S = wave_sum(part);
+        const unsigned long long last = so.entry[keep - 1];
+        f.inv_sum = 1.0 / S;
+        f.min_kept = key_logit(~(uint32_t)(last >> 32));
+        f.last = (int)(uint32_t)last;
+        f.n_kept = keep;
+        if (draw) {
+          // the kept entries by index
+          int q0 = 0, q1 = 0;
+#pragma unroll 8
+          for (int j = 0; j < keep; ++j) {
+            const uint32_t y = (uint32_t)so.entry[j];
+            q0 += y < (uint32_t)e[0];
+            q1 += y < (uint32_t)e[1];
+          }
+          if (k[0]) { so.w[q0] = w[0]; so.id[q0] = (int)(uint32_t)e[0]; }
+          if (k[1]) { so.w[q1] = w[1]; so.id[q1] = (int)(uint32_t)e[1]; }
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          double x[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) x[i] = 2 * l + i < keep ? so.w[2 * l + i] : 0.0;
+          const double at = wave_inclusive_scan(x[0] + x[1]);
+          const double goal = (double)u * __shfl(at, kWave - 1);
+          const double before = at - (x[0] + x[1]);
+          int first = INT32_MAX, any = -1;
+          if (x[0] > 0.0) { any = 2 * l; if (before + x[0] > goal) first = 2 * l; }
+          if (x[1] > 0.0) { any = 2 * l + 1; if (at > goal) first = min(first, 2 * l + 1); }
+#pragma unroll
+          for (int off = 32; off >= 1; off >>= 1) {
+            first = min(first, __shfl_xor(first, off));
+            any = max(any, __shfl_xor(any, off));
+          }
+          if (l == 0) sh.token = so.id[first == INT32_MAX ? any : first];
+        }
+      }
+    }
+    if (l == 0) {
+      sh.found = c;
+      sh.got = total;
+      sh.row = f;
+    }
+  }
+  __syncthreads();
+  f.inv_sum = uniform(sh.row.inv_sum);
+  f.min_kept = uniform(sh.row.min_kept);
+  f.last = uniform(sh.row.last);
+  f.n_kept = uniform(sh.row.n_kept);
+  got = uniform(sh.got);
+  return (ListCut)uniform(sh.found);
+}
+
+// The kept set of one row through the candidate list, and with `draw` the token
+// of uniform u.  Returns false where the row has to take the general path
+// (filter_row): more candidates than the list holds, or a large top-k.  The
+// candidates (the kept tokens and some more) stay in sh.list[0 .. count); count
+// is -1 for rows without a list, whose token is not drawn here.
 template <typename LT, int THREADS, bool PRE>
 __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, const LT* row, int V,
-                                                const FilterSettings& s, float* gm,
-                                                RowShared<THREADS>& sh, sv_filter_row& f,
-                                                int& count) {
+                                                const FilterSettings& s, bool draw, float u,
+                                                float* gm, RowShared<THREADS>& sh,
+                                                sv_filter_row& f, int& count) {
   const int G = group_octets(V);
   const int tiles = (V + kRowTile - 1) / kRowTile;
   const int groups = tiles * (8 / G) * kWave;
@@ -764,7 +1048,7 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
     low = block_reduce<THREADS>(low, reinterpret_cast<uint32_t*>(sh.redi), OpMin());
     f = sv_filter_row{s.c, 0.0, m, INFINITY, -1, 0};
     if (m == -INFINITY) { count = 0; return true; }
-    double S = 0.0;                                 // the sum of all weights
+    double S = -1.0;                                // the sum of all weights
     if (need_sum) {
       double part = 0.0;
 #pragma unroll 1
@@ -783,6 +1067,9 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
         return true;
       }
     }
+    // The fp32 sum's error: 2^-19 covers terms of |x| < 20; those below weigh
+    // under 2^-20.
+    const double slack = exact ? 0.0 : s.p * S * 0x1p-19;
     // the lowest key a kept token can have
     const uint32_t kmax = logit_key(m);
     uint32_t mp_key = kKeyNegInf + 1;
@@ -793,11 +1080,11 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
       mp_key = max(mp_key, min(kmax, logit_key(clean_logit(z)) - 2));
     }
     bool complete = true;                           // the list holds every kept token
-    bool ambiguous = false;
     double got = 0.0;
     uint32_t kt = kKeyNegInf + 1;
+    ListCut cut = CUT_SHORT;
 #pragma unroll 1
-    for (int attempt = 0;; ++attempt) {
+    for (int attempt = 0; attempt < 8; ++attempt) {
       if (!all) {
         if (by_k || nucleus) {
           // A nucleus row starts with the tokens of its kFirst largest groups,
@@ -811,7 +1098,7 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
               est ? (float)(1.1 * (s.p * S - got) / weight(z0, m, s.c, sh.table)) : 0.f;
           kt = s.k == 1 ? kmax
                         : threshold_key<THREADS>(gm, groups, est ? kt - 1 : kmax, low,
-                                                 est ? sh.nq : 0, z0, (float)s.c, k, aim, sh);
+                                                 est ? uniform(sh.nq) : 0, z0, (float)s.c, k, aim, sh);
           complete = !nucleus || kt <= mp_key;
           if (nucleus || s.p >= 1.0) kt = max(kt, mp_key);
         } else {
@@ -820,137 +1107,23 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
       }
       const int n = gather_tokens<LT, THREADS>(row, V, G, groups, gm, key_logit(kt), sh);
       if (n < 0) return false;
-      sort_list<THREADS>(sh, n);
-
-      // top-k, top-p and min-p along the order
-      const int nk = by_k ? min(n, s.k) : n;
-      const int chunk = (nk + THREADS - 1) / THREADS;
-      const int r0 = min((int)threadIdx.x * chunk, nk), r1 = min(r0 + chunk, nk);
-      const auto weight_of = [&](int i) {
-        return weight(key_logit(~(uint32_t)(sh.list[i] >> 32)), m, s.c, sh.table);
-      };
-      double part = 0.0, total;
-#pragma unroll 1
-      for (int i = r0; i < r1; ++i) part += weight_of(i);
-      double run = block_scan<THREADS>(part, sh.red, total);
-      const double target = s.p * (need_sum ? S : total);
-      // The fp32 sum's error: 2^-19 covers terms of |x| < 20; those below weigh
-      // under 2^-20.
-      const double slack = exact ? 0.0 : target * 0x1p-19;
-      if (!complete && total < target + slack) {
-        if (attempt == 7) return false;
-        got = total;
-        continue;
+      count = n;
+      cut = n <= kWaveList
+                ? cut_short_list<THREADS>(sh, n, s, m, S, slack, complete, draw, u, f, got)
+                : cut_list<LT, THREADS>(sh, n, s, V, m, S, slack, complete, draw, u, f, got);
+      if (cut != CUT_SHORT) break;
+    }
+    if (cut == CUT_SHORT) return false;
+    __syncthreads();
+    if (cut == CUT_DONE) {
+      if (s.off) {
+        f.min_kept = -INFINITY;
+        f.last = V - 1;
+        f.n_kept = V;
       }
-      int keep = 0, most = 0;
-      part = 0.0;
-#pragma unroll 1
-      for (int i = r0; i < r1; ++i) {
-        const double w = weight_of(i);
-        if (w >= s.mp) {
-          if (s.p >= 1.0 || run < target - slack) { ++keep; part += w; }
-          if (s.p >= 1.0 || run < target + slack) ++most;
-        }
-        run += w;
-      }
-      // both are at most kCand
-      const int both = block_reduce<THREADS>(most << 16 | keep, sh.redi, OpAdd());
-      keep = both & 0xffff;
-      ambiguous = keep != both >> 16;
-      if (ambiguous) break;
-      f.inv_sum = 1.0 / block_reduce<THREADS>(part, sh.red, OpAdd());
-      const unsigned long long last = sh.list[keep - 1];
-      f.min_kept = s.off ? -INFINITY : key_logit(~(uint32_t)(last >> 32));
-      f.last = s.off ? V - 1 : (int)(uint32_t)last;
-      f.n_kept = s.off ? V : keep;
-      count = keep;
       return true;
     }
-    __syncthreads();
   }
-}
-
-// The token drawn with uniform u from n <= N * THREADS entries in any order,
-// entry(i, token, mass).  The masses become integers, 2^50 to 2^51 the largest
-// (so that up to 4096 of them fit 64 bits and their sums do not depend on the
-// order of the additions); the token is found digit by digit, 8, 8 and 3 bits,
-// from the masses' sums per digit.  -1 if no entry has mass.  UNIT: the largest
-// mass is 1.
-template <int THREADS, int N, bool UNIT, typename F>
-__device__ __forceinline__ int draw_entries(int n, float u, unsigned long long* bucket, double* red,
-                                            F entry) {
-  static_assert(N * THREADS <= 4096, "sums fit 64 bits");
-  int id[N];
-  unsigned long long mass[N];
-  if constexpr (UNIT) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      id[j] = 0;
-      double x = 0.0;
-      if (j * THREADS + (int)threadIdx.x < n) entry(j * THREADS + threadIdx.x, id[j], x);
-      mass[j] = (unsigned long long)rint(x * 0x1p50);
-    }
-    __syncthreads();
-  } else {
-    double x[N], mx = 0.0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      id[j] = 0;
-      x[j] = 0.0;
-      if (j * THREADS + (int)threadIdx.x < n) entry(j * THREADS + threadIdx.x, id[j], x[j]);
-      mx = fmax(mx, x[j]);
-    }
-    mx = block_reduce<THREADS>(mx, red, OpMax());
-    if (!(mx > 0.0)) return -1;
-    const int up = 50 - ilogb(mx);
-#pragma unroll
-    for (int j = 0; j < N; ++j) mass[j] = (unsigned long long)rint(ldexp(x[j], up));
-  }
-  int prefix = 0;
-  double target = 0.0;                              // less what lies before the prefix
-  bool last = false;                                // rounding left no crossing
-#pragma unroll
-  for (int level = 0; level < 3; ++level) {
-    const int shift = level == 0 ? 11 : level == 1 ? 3 : 0;
-    const int bits = level == 2 ? 3 : 8;
-    for (int i = threadIdx.x; i < 256; i += THREADS) bucket[i] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (mass[j] && (id[j] >> (shift + bits)) == prefix)
-        atomicAdd(&bucket[(id[j] >> shift) & ((1 << bits) - 1)], mass[j]);
-    __syncthreads();
-    // every wave finds the same bucket
-    const int l = lane_id();
-    unsigned long long m[4], mine = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { m[i] = bucket[l * 4 + i]; mine += m[i]; }
-    unsigned long long run = mine;
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const unsigned long long y = __shfl_up(run, off);
-      if (l >= off) run += y;
-    }
-    if (level == 0) target = (double)u * (double)__shfl(run, kWave - 1);
-    run -= mine;
-    int hit = -1, any = -1;
-    unsigned long long before = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (m[i]) {
-        any = l * 4 + i;
-        if (hit < 0 && !last && (double)(run + m[i]) > target) { hit = l * 4 + i; before = run; }
-      }
-      run += m[i];
-    }
-    const unsigned long long hits = __ballot(hit >= 0), anys = __ballot(any >= 0);
-    last = last || !hits;
-    const int src = hits ? __ffsll((long long)hits) - 1 : 63 - __clzll((long long)anys);
-    prefix = prefix << bits | __shfl(hits ? hit : any, src);
-    target -= (double)__shfl(before, src);
-    __syncthreads();
-  }
-  return prefix;
 }
 
 // The tile in which the running total of the tiles' masses first exceeds
@@ -1056,8 +1229,37 @@ __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLau
   else stream_tile<LT, NO_SUM>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
 }
 
-template <typename LT, int THREADS, bool PRE>
-__global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
+// A row by the general path: the kept set by radix searches over the whole row,
+// the token by its tiles' masses.
+template <typename LT, int THREADS>
+__device__ __forceinline__ sv_filter_row general_row(const LT* row, int V, const FilterSettings& s,
+                                                     bool draw, float u, unsigned char* lds,
+                                                     int& token) {
+  __syncthreads();
+  const sv_filter_row f =
+      filter_row<LT, THREADS>(row, V, s, *reinterpret_cast<FilterShared<THREADS>*>(lds));
+  token = 0;                                        // of an empty row
+  if (draw && f.n_kept > 0)
+    token = block_draw<THREADS>(V, u, *reinterpret_cast<DrawShared*>(lds), [&](int e) {
+      const float z = clean_logit(logit_at(row, e));
+      return row_keeps(f, z, e) ? weight(z, f.max, f.scale) : 0.0;
+    });
+  return f;
+}
+
+// The dense q of a row from its filter row alone.
+template <typename LT, int THREADS>
+__device__ __forceinline__ void write_probs(const LT* row, int V, const sv_filter_row& f, float* q) {
+  for (int e = threadIdx.x; e < V; e += THREADS)
+    __builtin_nontemporal_store((float)row_prob(f, logit_at(row, e), e), q + e);
+}
+
+// One workgroup per row.  PRE: the row was streamed by filter_stream_kernel.
+// GENERAL: rows for the general path are done here, which costs registers and
+// spares a launch; otherwise they are left to filter_general_kernel.
+template <typename LT, int THREADS, bool PRE, bool GENERAL>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4))) void
+filter_rows_kernel(FilterLaunch A) {
   extern __shared__ __align__(16) unsigned char lds[];
   RowShared<THREADS>& sh = *reinterpret_cast<RowShared<THREADS>*>(lds);
   float* gm = reinterpret_cast<float*>(lds + sizeof(RowShared<THREADS>));
@@ -1071,41 +1273,43 @@ __global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
   const bool there = ri >= 0 && ri < A.n_rows;
   sv_filter_row f{0.0, 0.0, -INFINITY, INFINITY, -1, 0};
   const LT* row = static_cast<const LT*>(A.logits) + (there ? ri : 0) * A.row_stride;
+  const bool sampled = A.out_tokens && s.c != 0.0;
+  const float u = sampled ? A.uniforms[r] : 0.f;
   fill_exp_table(sh.table, threadIdx.x, THREADS);
   if (A.pending && r == 0 && threadIdx.x == 0) *A.pending = 0;
   __syncthreads();
-  int count = 0;                                    // entries in sh.list; -1: no list
-  if (there && !filter_row_list<LT, THREADS, PRE>(A, r, row, V, s, gm, sh, f, count)) {
-    if (threadIdx.x == 0) A.list_counts[r] = kGeneralRow;
-    return;
+  int count = 0;                                    // candidates in sh.list; -1: no list
+  int token = there ? 0 : -1;
+  if (there) {
+    if (filter_row_list<LT, THREADS, PRE>(A, r, row, V, s, sampled, u, gm, sh, f, count)) {
+      if (f.n_kept > 0) {
+        if (s.c == 0.0) token = f.last;
+        else if (!sampled) token = 0;
+        else if (count >= 0) token = sh.token;
+        else token = draw_tiles<LT, THREADS>(row, V, sh, u, f.max, s.c);
+      }
+    } else {
+      if constexpr (!GENERAL) {
+        if (threadIdx.x == 0) A.list_counts[r] = kGeneralRow;
+        return;
+      } else {
+        f = general_row<LT, THREADS>(row, V, s, sampled, u, lds, token);
+        if (s.c == 0.0 && f.n_kept > 0) token = f.last;
+        count = -1;
+      }
+    }
   }
   if (!there) errors |= SV_DEVERR_ROW_INDEX;
   else if (f.n_kept == 0) errors |= SV_DEVERR_EMPTY_ROW;
   if (threadIdx.x == 0) {
     if (errors) flag_error(A.device_error, errors);
     if (A.out_rows) A.out_rows[r] = f;
-    if (A.list_counts) A.list_counts[r] = count;
+    A.list_counts[r] = count;
+    if (A.out_tokens) A.out_tokens[r] = token;
   }
   if (A.lists)
     for (int i = threadIdx.x; i < count; i += THREADS)
       A.lists[r * kCand + i] = (int32_t)(uint32_t)sh.list[i];
-  if (A.out_tokens) {
-    int token = there ? 0 : -1;
-    if (f.n_kept > 0) {
-      if (s.c == 0.0) token = f.last;
-      else if (count > 0)
-        token = draw_entries<THREADS, kCand / THREADS, true>(
-            count, A.uniforms[r], sh.bucket, sh.red, [&](int i, int& id, double& mass) {
-              const unsigned long long x = sh.list[i];
-              const float z = key_logit(~(uint32_t)(x >> 32));
-              id = (int)(uint32_t)x;
-              mass = row_keeps(f, z, id) ? weight(z, f.max, f.scale, sh.table) : 0.0;
-            });
-      else
-        token = draw_tiles<LT, THREADS>(row, V, sh, A.uniforms[r], f.max, s.c);
-    }
-    if (threadIdx.x == 0) A.out_tokens[r] = token;
-  }
   if (A.out_probs) {
     float* q = A.out_probs + r * V;
     if (count >= 0) {
@@ -1118,23 +1322,20 @@ __global__ __launch_bounds__(THREADS) void filter_rows_kernel(FilterLaunch A) {
           q[(uint32_t)x] = (float)(weight(z, f.max, f.scale, sh.table) * f.inv_sum);
       }
     } else {
-      for (int e = threadIdx.x; e < V; e += THREADS)
-        __builtin_nontemporal_store(
-            (float)(weight(clean_logit(logit_at(row, e)), f.max, f.scale, sh.table) * f.inv_sum), q + e);
+      write_probs<LT, THREADS>(row, V, f, q);
     }
   }
 }
 
-// The rows that filter_rows_kernel left (their counts say so): every filter by
-// a radix search over the whole row, one workgroup per row in turn.
+// The rows that filter_rows_kernel left (their counts say so), one workgroup
+// per row in turn.
 constexpr int kGeneralThreads = 1024;
 template <typename LT>
 __global__ __launch_bounds__(kGeneralThreads) void filter_general_kernel(FilterLaunch A) {
   constexpr int THREADS = kGeneralThreads;
-  __shared__ union {
-    FilterShared<THREADS> filter;
-    DrawShared draw;
-  } sh;
+  __shared__ __align__(16) unsigned char
+      lds[sizeof(FilterShared<THREADS>) > sizeof(DrawShared) ? sizeof(FilterShared<THREADS>)
+                                                             : sizeof(DrawShared)];
   const int V = A.V;
   const long rows = (long)A.B * A.per_seq;
   for (long r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -1144,27 +1345,20 @@ __global__ __launch_bounds__(kGeneralThreads) void filter_general_kernel(FilterL
                                              A.min_ps, (int)(r / A.per_seq), V, errors);
     const LT* row = static_cast<const LT*>(A.logits) +
                     (A.row_index ? (long)A.row_index[r] : r) * A.row_stride;
-    __syncthreads();                                // the last row's draw, and every read of its count
-    const sv_filter_row f = filter_row<LT, THREADS>(row, V, s, sh.filter);
+    const bool sampled = A.out_tokens && s.c != 0.0;
+    // a barrier before anything is written: every thread has read the count
+    int token;
+    const sv_filter_row f = general_row<LT, THREADS>(
+        row, V, s, sampled, sampled ? A.uniforms[r] : 0.f, lds, token);
     if (f.n_kept == 0) errors |= SV_DEVERR_EMPTY_ROW;
+    else if (s.c == 0.0) token = f.last;
     if (threadIdx.x == 0) {
       if (errors) flag_error(A.device_error, errors);
       if (A.out_rows) A.out_rows[r] = f;
+      if (A.out_tokens) A.out_tokens[r] = token;
       A.list_counts[r] = -1;
     }
-    if (A.out_tokens) {
-      // an empty row has no mass: token 0
-      const int token = f.n_kept == 0 ? 0 : block_draw<THREADS>(V, A.uniforms[r], sh.draw, [&](int e) {
-        const float z = clean_logit(logit_at(row, e));
-        return row_keeps(f, z, e) ? weight(z, f.max, f.scale) : 0.0;
-      });
-      if (threadIdx.x == 0) A.out_tokens[r] = token;
-    }
-    if (A.out_probs) {
-      float* q = A.out_probs + r * V;
-      for (int e = threadIdx.x; e < V; e += THREADS)
-        __builtin_nontemporal_store((float)row_prob(f, logit_at(row, e), e), q + e);
-    }
+    if (A.out_probs) write_probs<LT, THREADS>(row, V, f, A.out_probs + r * V);
   }
 }
 
@@ -1199,6 +1393,8 @@ template <typename LT, bool QL>
 __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(FilteredVerifyLaunch A) {
   __shared__ double red[kVerifyThreads / kWave];
   __shared__ unsigned long long bucket[256];
+  __shared__ double mass[kCand];
+  __shared__ int id[kCand];
   __shared__ int sh_a;
   const int b = blockIdx.x, K = A.K, V = A.V;
   const int l = lane_id();
@@ -1250,22 +1446,45 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
       return;
     }
     const int32_t* list = A.lists + (row0 + a) * kCand;
-    token = -1;
+    // the residual's masses, and p's
+    const auto each = [&](auto f) {
+      for (int i = threadIdx.x; i < count; i += kVerifyThreads) f(i);
+    };
+    double most = 0.0;
+    each([&](int i) {
+      const int x = list[i];
+      id[i] = x;
+      mass[i] = row_prob(f, logit_at(za, x), x);
+    });
     if (a < K) {
       const DrafterQ<LT, QL> q(A, b, a);
-      token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
-          count, u, bucket, red, [&](int i, int& id, double& mass) {
-            id = list[i];
-            const double p = row_prob(f, logit_at(za, id), id);
-            mass = p > 0.0 ? fmax(0.0, p - q.at(id)) : 0.0;
-          });
+      each([&](int i) {
+        if (mass[i] > 0.0) most = fmax(most, mass[i] - q.at(id[i]));
+      });
+      most = block_reduce<kVerifyThreads>(most, red, OpMax());
+      if (most > 0.0)
+        each([&](int i) {
+          mass[i] = mass[i] > 0.0 ? fmax(0.0, mass[i] - q.at(id[i])) : 0.0;
+        });
     }
-    if (token < 0)                                   // a = K, or q covers p
-      token = draw_entries<kVerifyThreads, kCand / kVerifyThreads, false>(
-          count, u, bucket, red, [&](int i, int& id, double& mass) {
-            id = list[i];
-            mass = row_prob(f, logit_at(za, id), id);
-          });
+    if (!(most > 0.0)) {                             // a = K, or q covers p
+      each([&](int i) { most = fmax(most, mass[i]); });
+      most = block_reduce<kVerifyThreads>(most, red, OpMax());
+    }
+    // as integers, the largest between 2^50 and 2^51
+    const int up = 50 - ilogb(most);
+    unsigned long long total = 0, before, inside;
+    each([&](int i) {
+      const unsigned long long x = (unsigned long long)rint(ldexp(mass[i], up));
+      mass[i] = __longlong_as_double(x);
+      total += x;
+    });
+    total = block_reduce<kVerifyThreads>(total, reinterpret_cast<unsigned long long*>(red), OpAdd());
+    __syncthreads();
+    token = (int)digit_search<kVerifyThreads, 19, true>(
+        count, [&](int i) { return (uint32_t)id[i]; },
+        [&](int i) { return (unsigned long long)__double_as_longlong(mass[i]); },
+        (double)u * (double)total, bucket, before, inside);
   }
   if (threadIdx.x == 0) A.out_tokens[row0 + a] = token;
 }
@@ -1370,8 +1589,10 @@ __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerify
 
 namespace {
 
-// Rows whose stream gets a kernel of its own, spread over all CUs.
-bool streams_apart(long rows, int V) { return V > kCand && rows <= 512; }
+// Few rows take workgroups of 512 threads; where they are long, their stream
+// gets a kernel of its own, spread over all CUs.
+bool few_rows(long rows) { return rows <= 512; }
+bool streams_apart(long rows, int V) { return few_rows(rows) && V > 16 * kRowTile; }
 
 // The parts of the workspace, in order; each starts at a multiple of 16 bytes.
 struct FilterWorkspace {
@@ -1402,12 +1623,13 @@ struct FilterWorkspace {
   }
 };
 
-template <typename LT, int THREADS, bool PRE>
+template <typename LT, int THREADS, bool PRE, bool GENERAL>
 void launch_rows(const FilterLaunch& L, hipStream_t stream) {
   const int tiles = (L.V + kRowTile - 1) / kRowTile;
   const size_t gm = (size_t)tiles * (8 / group_octets(L.V)) * kWave * sizeof(float);
-  const size_t lds = sizeof(RowShared<THREADS>) + gm;
-  filter_rows_kernel<LT, THREADS, PRE>
+  const size_t lds =
+      std::max(sizeof(RowShared<THREADS>) + gm, GENERAL ? sizeof(FilterShared<THREADS>) : 0);
+  filter_rows_kernel<LT, THREADS, PRE, GENERAL>
       <<<dim3((unsigned)((long)L.B * L.per_seq)), THREADS, lds, stream>>>(L);
 }
 
@@ -1423,19 +1645,17 @@ hipError_t launch_filter(const FilterLaunch& L, hipStream_t stream) {
     trace_after(stream, SV_KERNEL_FILTER_ROWS);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    trace_before(stream, SV_KERNEL_FILTER_ROWS);
-    launch_rows<LT, 512, true>(L, stream);
-    trace_after(stream, SV_KERNEL_FILTER_ROWS);
-  } else {
-    trace_before(stream, SV_KERNEL_FILTER_ROWS);
-    launch_rows<LT, 256, false>(L, stream);
-    trace_after(stream, SV_KERNEL_FILTER_ROWS);
   }
+  trace_before(stream, SV_KERNEL_FILTER_ROWS);
+  if (streams_apart(rows, L.V)) launch_rows<LT, 512, true, true>(L, stream);
+  else if (few_rows(rows)) launch_rows<LT, 512, false, true>(L, stream);
+  else launch_rows<LT, 256, false, false>(L, stream);
+  trace_after(stream, SV_KERNEL_FILTER_ROWS);
   hipError_t e = hipGetLastError();
   // every token of a short row fits the list
-  if (e == hipSuccess && L.V > kCand) {
+  if (e == hipSuccess && !few_rows(rows) && L.V > kCand) {
     trace_before(stream, SV_KERNEL_FILTER_ROWS);
-    filter_general_kernel<LT><<<dim3((unsigned)std::min(rows, 256L)), kGeneralThreads, 0, stream>>>(L);
+    filter_general_kernel<LT><<<dim3(256), kGeneralThreads, 0, stream>>>(L);
     trace_after(stream, SV_KERNEL_FILTER_ROWS);
     e = hipGetLastError();
   }
