@@ -10,6 +10,7 @@
 //                        the filter rows, then the residual draw on the row
 //                        of the first rejection.
 #include <algorithm>
+#include <type_traits>
 
 #include "sv_filter.h"
 #include "sv_internal.h"
@@ -328,19 +329,23 @@ __device__ __forceinline__ sv_filter_row filter_row(const LT* row, int V, const 
 
 // ---------------------------------------------------------------- one pass over a row
 // The logits are streamed once.  A wave takes tiles of 4096 elements, lane l
-// the octets u = 0..7 at 512 u + 8 l of a tile; every G octets of a lane are a
-// group, whose maximum goes to LDS (V / (8 G) of them).  The group maxima are
-// logits of the row, so the k-th largest of them is a lower bound of its k-th
-// largest logit: only groups whose maximum reaches a threshold found among
-// them (candidate groups) can hold kept tokens, and only those are read again.
-// Where a filter needs the row's whole sum (top-p without top-k, no filter at
-// all) the pass also leaves every tile's maximum and sum of weights.
+// the octets u = 0..7 at 512 u + 8 l of a tile; G adjacent octets are a group,
+// whose maximum goes to LDS (V / (8 G) of them).  The group maxima are logits
+// of the row, so the k-th largest of them is a lower bound of its k-th largest
+// logit: only groups whose maximum reaches a threshold found among them
+// (candidate groups) can hold kept tokens, and only those are read again, one
+// or two lines of memory each.  Where a filter needs the row's whole sum (top-p
+// without top-k, no filter at all) the pass also leaves every tile's maximum
+// and sum of weights.
 constexpr int kRowTile = 4096;
 constexpr int kRowTiles = SV_MAX_V / kRowTile;
-constexpr int kCand = 2048;            // candidate tokens a workgroup sorts in LDS
+constexpr int kCand = 2048;            // candidate tokens of a row's list in the workspace, and in
+                                       // LDS where many rows are worked on
+constexpr int kCandFew = 4096;         // ... in LDS elsewhere
 constexpr int kQueue = 2048;           // candidate groups
+constexpr int kBuckets = 512;          // of a digit search
 constexpr int kTopBins = 256;          // histogram of the group maxima
-constexpr int kFirst = 96;             // groups whose tokens a nucleus row looks at first
+constexpr int kFirst = 96;             // groups a nucleus row falls back to
 constexpr int kGeneralRow = -2;        // list_counts: the row takes the general path
 constexpr int kMaxListK = 1024;        // largest top-k taken through the candidate list
 constexpr int kWaveList = 128;         // most candidates that one wave cuts and draws from
@@ -353,18 +358,19 @@ __host__ __device__ __forceinline__ int group_octets(int V) {
 
 template <int THREADS>
 struct RowShared {
-  unsigned long long list[kCand];      // candidates: order_entry
   union {
     struct { uint32_t cnt[kTopBins], mass[kTopBins]; } top;
     uint16_t queue[kQueue];
-    unsigned long long bucket[256];
+    unsigned long long bucket[kBuckets];
     struct { unsigned long long entry[kWaveList]; double w[kWaveList]; int id[kWaveList]; } sorted;
   };
   double tile_s[kRowTiles];
   float tile_m[kRowTiles];
   double table[kExpTable];
-  double red[THREADS / kWave];
+  double red[3 * (THREADS / kWave)];
   int redi[THREADS / kWave];
+  unsigned long long* list;            // candidates: order_entry; cap of them at most
+  int cap;
   int n, nq, token, bin, above;
   float frac;
   // what the first wave finds in a short list
@@ -403,18 +409,32 @@ __device__ __forceinline__ bool row_needs_sum(const FilterSettings& s, int V) {
 // How the stream takes it.
 enum RowSum { NO_SUM, SUM_F32, SUM_F64 };
 
+// The maximum over N = 2, 4 or 8 adjacent lanes (from the maximum over N / 2,
+// for N = 4; the whole for N = 8).
+template <int N>
+__device__ __forceinline__ float max_adjacent(float x) {
+  const auto other = [&](auto dpp) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x),
+                                                      decltype(dpp)::value, 0xf, 0xf, false));
+  };
+  if constexpr (N != 4) x = fmaxf(x, other(std::integral_constant<int, 0xB1>()));   // 1 0 3 2
+  if constexpr (N != 2) x = fmaxf(x, other(std::integral_constant<int, 0x4E>()));   // 2 3 0 1
+  if constexpr (N == 8) x = fmaxf(x, other(std::integral_constant<int, 0x141>()));  // 7 .. 0
+  return x;
+}
+
 // One wave's tile t of a row: its groups' maxima to gm (the row's), with a sum
 // its maximum and sum of weights to *tile_m, *tile_s.  Gives the lane's largest
-// logit and its groups' lowest key above -inf.  128 bytes a lane are in flight:
+// logit.  128 bytes a lane are in flight:
 // a bf16 tile at once, an fp32 tile in two parts.
 template <typename LT, RowSum SUM>
 __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double c, int G, float* gm,
                                             float* tile_m, double* tile_s, const double* table,
-                                            float& top, uint32_t& low) {
+                                            float& top) {
   constexpr int OCTS = 16 / sizeof(LT);
   const int l = lane_id();
-  const int per = 8 / G;
-  float g = -INFINITY, ref = -INFINITY;             // ref: the sum's reference logit
+  float ref = -INFINITY;                            // the sum's reference logit
+  float mine = -INFINITY;                           // G = 8: the maximum of octet l & 7's group
   double sum = 0.0;
 #pragma unroll 1
   for (int part = 0; part < 8 / OCTS; ++part) {
@@ -436,17 +456,18 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
     for (int u = 0; u < OCTS; ++u) {
       float z[8];
       unpack(raw[u], z);
-      g = fmaxf(g, fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])),
-                         fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7]))));
-      if (((u + 1) & (G - 1)) == 0 || u + 1 == OCTS) {   // uniform
-        g = clean_logit(g);
-        mt = fmaxf(mt, g);
-        const int o = part * OCTS + u + 1;
-        if ((o & (G - 1)) == 0) {                   // a group ends
-          gm[(t * per + (o - 1) / G) * kWave + l] = g;
-          if (g > -INFINITY) low = min(low, logit_key(g));
-          g = -INFINITY;
-        }
+      float g = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])),
+                      fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+      g = clean_logit(g);
+      mt = fmaxf(mt, g);
+      if (G == 8) {                                 // uniform
+        g = max_adjacent<8>(g);
+        mine = (l & 7) == part * OCTS + u ? g : mine;
+      } else {
+        if (G >= 2) g = max_adjacent<2>(g);
+        if (G >= 4) g = max_adjacent<4>(g);
+        if ((l & (G - 1)) == 0)
+          gm[(t * (kRowTile / 8) + (part * OCTS + u) * kWave + l) / G] = g;
       }
     }
     top = fmaxf(top, mt);
@@ -505,6 +526,7 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
       if (mt > -INFINITY) sum += s * weight(mt, ref, c, table);
     }
   }
+  if (G == 8) gm[t * kWave + (l & 7) * 8 + (l >> 3)] = mine;
   if constexpr (SUM != NO_SUM)
     if (l == 0) { *tile_m = ref; *tile_s = sum; }
 }
@@ -512,23 +534,22 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
 // A whole row by one workgroup, into LDS.
 template <typename LT, int THREADS, RowSum SUM>
 __device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G, float* gm,
-                                           RowShared<THREADS>& sh, float& top, uint32_t& low) {
+                                           RowShared<THREADS>& sh, float& top) {
   const int tiles = (V + kRowTile - 1) / kRowTile;
   for (int t = threadIdx.x / kWave; t < tiles; t += THREADS / kWave)
-    stream_tile<LT, SUM>(row, V, t, c, G, gm, &sh.tile_m[t], &sh.tile_s[t], sh.table, top, low);
+    stream_tile<LT, SUM>(row, V, t, c, G, gm, &sh.tile_m[t], &sh.tile_s[t], sh.table, top);
 }
 
 // What a row's stream leaves, where a kernel of its own made it: into LDS.
 template <int THREADS>
 __device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int groups, int tiles,
                                               bool sum, float* gm, RowShared<THREADS>& sh,
-                                              float& top, uint32_t& low) {
+                                              float& top) {
   const float* g = A.group_max + r * groups;
   for (int i = threadIdx.x; i < groups; i += THREADS) {
     const float x = g[i];
     gm[i] = x;
     top = fmaxf(top, x);
-    if (x > -INFINITY) low = min(low, logit_key(x));
   }
   if (sum)
     for (int t = threadIdx.x; t < tiles; t += THREADS) {
@@ -544,19 +565,20 @@ __device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int
 // wide.  A maximum stands for the group's tokens of its own size; in the
 // estimate of the mass, those hidden behind a larger one of their group are
 // added as 1 / (share of groups without a larger one).  The search starts at
-// key `hi`, `above` groups lying above it.
+// key `hi`, `above` groups lying above it; the lowest finite key if nothing
+// reaches it.
 template <int THREADS>
 __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, uint32_t hi,
-                                                  uint32_t lo, int above, float z0, float c, int k,
+                                                  int above, float z0, float c, int k,
                                                   float aim, RowShared<THREADS>& sh) {
   const bool by_mass = k == 0;
-  if (hi < lo) return kKeyNegInf + 1;
+  constexpr uint32_t FLOOR = kKeyNegInf + 1;
+  if (hi < FLOOR) return FLOOR;
   float mass = 0.f;                    // estimated mass found
-  // by count, a binade below the maximum first: the threshold of a row's largest
-  // logits is mostly there, in narrow bins
-  const uint32_t floor = lo;
-  bool near = !by_mass && hi - lo > 0x800000u;
-  if (near) lo = hi - 0x800000u;
+  // a binade first: the threshold of a row's largest logits is mostly there, in
+  // narrow bins
+  bool near = hi - FLOOR > 0x800000u;
+  uint32_t lo = near ? hi - 0x800000u : FLOOR;
 #pragma unroll 1
   for (int level = 0; level < 5; ++level) {
     // hi - lo < 256 << shift
@@ -642,12 +664,12 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
     if (b < 0) {
       if (near) {                                   // not within the binade
         near = false;
-        lo = floor;
+        lo = FLOOR;
         continue;
       }
       // not reached: every token, or (by mass, inside a bin that seemed to
       // reach it) what there is
-      return lo == floor ? kKeyNegInf + 1 : lo;
+      return lo;
     }
     near = false;
     above = uniform(sh.above);
@@ -669,7 +691,6 @@ template <typename LT, int THREADS>
 __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int groups,
                                              const float* gm, float zt,
                                              RowShared<THREADS>& sh) {
-  const int per = 8 / G;
   __syncthreads();
   if (threadIdx.x == 0) { sh.nq = 0; sh.n = 0; }
   __syncthreads();
@@ -682,22 +703,22 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
   __syncthreads();
   const int nq = uniform(sh.nq);
   if (nq > kQueue) return -1;
-  // four octets a thread at a time, to have their loads in flight together
+  // 64 bytes a thread at a time, to have their loads in flight together
+  constexpr int BATCH = 8 / sizeof(LT);
   const int items = nq * G;
 #pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < items; i0 += 4 * THREADS) {
-    Raw<LT> raw[4];
-    int e[4];
+  for (int i0 = threadIdx.x; i0 < items; i0 += BATCH * THREADS) {
+    Raw<LT> raw[BATCH];
+    int e[BATCH];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < BATCH; ++p) {
       const int i = min(i0 + p * THREADS, items - 1);
-      const int q = sh.queue[i / G], u = q / kWave % per * G + i % G;
-      e[p] = q / (per * kWave) * kRowTile + u * kTile + q % kWave * 8;
+      e[p] = (sh.queue[i / G] * G + i % G) * 8;
       if (e[p] + 8 <= V) raw8(row + e[p], raw[p]);
       else raw8_end(row, e[p], V, raw[p]);
     }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < BATCH; ++p) {
       if (i0 + p * THREADS >= items) break;
       float z[8];
       unpack(raw[p], z);
@@ -706,50 +727,63 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
         const float x = clean_logit(z[j]);
         if (x >= zt) {
           const int at = atomicAdd(&sh.n, 1);
-          if (at < kCand) sh.list[at] = order_entry(logit_key(x), e[p] + j);
+          if (at < sh.cap) sh.list[at] = order_entry(logit_key(x), e[p] + j);
         }
       }
     }
   }
   __syncthreads();
   const int n = uniform(sh.n);
-  return n > kCand ? -1 : n;
+  return n > sh.cap ? -1 : n;
 }
 
-// Search of a running total over n numbers, digit by digit (8 bits, most
-// significant first): the smallest key(i) of BITS bits at which the sum of x(i)
+// Search of a running total over n numbers, digit by digit (9 bits, most
+// significant first): the smallest key(i) of `bits` bits at which the sum of x(i)
 // over the keys up to it reaches target (STRICT: exceeds it), or the largest key
 // with x > 0 if none does.  x are integers, so the sums do not depend on the
 // order in which LDS adds them.  Also the sums over smaller keys and over that
 // key.  Workgroup-wide; thread t sees the numbers t, t + THREADS, ...
-template <int THREADS, int BITS, bool STRICT, typename K, typename X>
-__device__ __forceinline__ uint32_t digit_search(int n, K key, X x, double target,
+template <int THREADS, bool STRICT, typename K, typename X>
+__device__ __forceinline__ uint32_t digit_search(int n, int bits, K key, X x, double target,
                                                  unsigned long long* bucket,
                                                  unsigned long long& before,
                                                  unsigned long long& inside) {
+  constexpr int DIGIT = 9, PER = kBuckets / kWave;
+  static_assert(kBuckets == 1 << DIGIT, "a bucket per digit");
   uint32_t prefix = 0;
   before = inside = 0;
   bool past = false;                                // no crossing: the last key
 #pragma unroll 1
-  for (int rest = BITS; rest > 0;) {
-    const int bits = rest < 8 ? rest : 8;
-    const int shift = rest - bits;
-    for (int i = threadIdx.x; i < 256; i += THREADS) bucket[i] = 0;
+  for (int rest = bits; rest > 0;) {
+    const int now = min(rest, DIGIT), shift = rest - now;
+    for (int i = threadIdx.x; i < kBuckets; i += THREADS) bucket[i] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < n; i += THREADS) {
       const uint32_t d = key(i);
-      if (rest == 32 || d >> rest == prefix) {
+      if (rest == bits || d >> rest == prefix) {
         const unsigned long long v = x(i);
-        if (v) atomicAdd(&bucket[(d >> shift) & ((1u << bits) - 1)], v);
+        if (v) atomicAdd(&bucket[(d >> shift) & ((1u << now) - 1)], v);
       }
     }
     __syncthreads();
-    // every wave finds the same bucket
+    // every wave finds the same bucket: the lane whose eight buckets hold it,
+    // then the bucket among those, a lane each
     const int l = lane_id();
-    unsigned long long m[4], mine = 0;
+    const auto over = [&](unsigned long long sum) {
+      return STRICT ? (double)sum > target : (double)sum >= target;
+    };
+    const auto find = [&](unsigned long long x, unsigned long long& run) {
+      // the first lane at whose x the total is over the target, else the last with any
+      const unsigned long long hits = __ballot(x && !past && over(run + x)), any = __ballot(x != 0);
+      const int src = hits ? __ffsll((long long)hits) - 1 : any ? 63 - __clzll((long long)any) : 0;
+      past = past || !hits;
+      run = uniform(__shfl(run, src));
+      return src;
+    };
+    unsigned long long mine = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { m[i] = bucket[l * 4 + i]; mine += m[i]; }
+    for (int i = 0; i < PER; ++i) mine += bucket[l * PER + i];
     unsigned long long run = mine;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
@@ -757,31 +791,26 @@ __device__ __forceinline__ uint32_t digit_search(int n, K key, X x, double targe
       if (l >= off) run += y;
     }
     run += before - mine;
-    int hit = -1, any = -1;
-    unsigned long long at = 0, in = 0, any_at = 0, any_in = 0;
+    const int lane = find(mine, run);
+    const unsigned long long x8 = l < PER ? bucket[lane * PER + l] : 0;
+    unsigned long long in = x8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned long long next = run + m[i];
-      if (m[i]) {
-        any = l * 4 + i;
-        any_at = run;
-        any_in = m[i];
-        const bool over = STRICT ? (double)next > target : (double)next >= target;
-        if (hit < 0 && over && !past) { hit = l * 4 + i; at = run; in = m[i]; }
-      }
-      run = next;
+    for (int off = 1; off < PER; off <<= 1) {
+      const unsigned long long y = __shfl_up(in, off);
+      if (l >= off) in += y;
     }
-    const unsigned long long hits = __ballot(hit >= 0), anys = __ballot(any >= 0);
-    past = past || !hits;
-    const int src = hits ? __ffsll((long long)hits) - 1 : anys ? 63 - __clzll((long long)anys) : 0;
-    prefix = prefix << bits | uniform((uint32_t)__shfl(hits ? hit : any, src));
-    before = uniform(__shfl(hits ? at : any_at, src));
-    inside = uniform(__shfl(hits ? in : any_in, src));
+    run += in - x8;
+    const int at = find(x8, run);
+    prefix = prefix << now | (uint32_t)(lane * PER + at);
+    before = run;
+    inside = uniform(__shfl(x8, at));
     __syncthreads();
-    rest -= bits;
+    rest -= now;
   }
   return prefix;
 }
+// Bits of the numbers 0 .. x, at least 1.
+__device__ __forceinline__ int bits_of(uint32_t x) { return 32 - __clz((int)(x | 1u)); }
 
 // What a list's cut came to.
 enum ListCut { CUT_DONE, CUT_SHORT, CUT_AMBIGUOUS };
@@ -803,17 +832,21 @@ __device__ __forceinline__ int ties_below(double target, double before, double w
 // bits and are exact whatever their order).
 template <typename LT, int THREADS>
 __device__ __forceinline__ ListCut cut_list(RowShared<THREADS>& sh, int n, const FilterSettings& s,
-                                            int V, float m, double sum, double slack, bool complete,
-                                            bool draw, float u, sv_filter_row& f, double& got) {
-  static_assert(kCand <= 32 * THREADS, "a bit per entry of a thread");
+                                            int V, float m, uint32_t kt, double sum, double slack,
+                                            bool complete, bool draw, float u, sv_filter_row& f,
+                                            double& got) {
+  static_assert(kCandFew <= 32 * 512 && kCand <= 32 * 256, "a bit per entry of a thread");
   constexpr double UNIT = 0x1p50;
-  // bf16 keys differ in their upper halves only
-  constexpr int KEY_BITS = sizeof(LT) == 2 ? 16 : 32;
+  constexpr int W = THREADS / kWave;
   unsigned kept = ~0u;                              // bit i / THREADS: entry i
   const auto is_kept = [&](int i) { return (kept >> (i / THREADS)) & 1u; };
   const auto drop = [&](int i) { kept &= ~(1u << (i / THREADS)); };
-  // ~key: increases along the order
-  const auto digits = [&](int i) { return (uint32_t)(sh.list[i] >> (64 - KEY_BITS)); };
+  // how far below the maximum's a key lies: increases along the order; bf16
+  // keys differ in their upper halves only
+  constexpr int LOW = sizeof(LT) == 2 ? 16 : 0;
+  const uint32_t kmax = logit_key(m) >> LOW;
+  const int key_bits = bits_of(kmax - (kt >> LOW)), id_bits = bits_of((uint32_t)(V - 1));
+  const auto digits = [&](int i) { return kmax - (~(uint32_t)(sh.list[i] >> 32) >> LOW); };
   const auto id = [&](int i) { return (uint32_t)sh.list[i]; };
   const auto weight_of = [&](int i) {
     return weight(key_logit(~(uint32_t)(sh.list[i] >> 32)), m, s.c, sh.table);
@@ -833,65 +866,94 @@ __device__ __forceinline__ ListCut cut_list(RowShared<THREADS>& sh, int n, const
     uint32_t last = 0xffffffffu;
     if (keep < ties) {
       unsigned long long x, y;
-      last = digit_search<THREADS, 19, false>(
-          n, id, [&](int i) { return digits(i) == d ? one(i) : 0ull; }, (double)keep, sh.bucket, x,
-          y);
+      last = digit_search<THREADS, false>(
+          n, id_bits, id, [&](int i) { return digits(i) == d ? one(i) : 0ull; }, (double)keep,
+          sh.bucket, x, y);
     }
     each([&](int i) {
       const uint32_t e = digits(i);
       if (e > d || (e == d && id(i) > last)) drop(i);
     });
   };
+  // sum, sum and maximum over the workgroup, in one go
+  const auto reduce = [&](unsigned long long& a, unsigned long long& b, unsigned long long& c) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      a += __shfl_xor(a, off);
+      b += __shfl_xor(b, off);
+      c = max(c, __shfl_xor(c, off));
+    }
+    unsigned long long* red = reinterpret_cast<unsigned long long*>(sh.red);
+    __syncthreads();
+    if (lane_id() == 0) {
+      const int w = threadIdx.x / kWave;
+      red[w] = a;
+      red[W + w] = b;
+      red[2 * W + w] = c;
+    }
+    __syncthreads();
+    a = red[0];
+    b = red[W];
+    c = red[2 * W];
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      a += red[i];
+      b += red[W + i];
+      c = max(c, red[2 * W + i]);
+    }
+    a = uniform(a);
+    b = uniform(b);
+    c = uniform(c);
+  };
   __syncthreads();                                  // the queue is read, the list written
   if (s.k < n) {
-    const uint32_t d = digit_search<THREADS, KEY_BITS, false>(n, digits, one, (double)s.k,
-                                                               sh.bucket, before, inside);
+    const uint32_t d =
+        digit_search<THREADS, false>(n, key_bits, digits, one, (double)s.k, sh.bucket, before, inside);
     cut_at(d, s.k - (int)before, (int)inside);
   }
-  const auto total_mass = [&]() {
-    unsigned long long x = 0;
-    each([&](int i) { x += mass(i); });
-    return block_reduce<THREADS>(x, reinterpret_cast<unsigned long long*>(sh.red), OpAdd());
-  };
-  unsigned long long total = total_mass();
-  got = (double)total / UNIT;
   if (s.p < 1.0) {
+    unsigned long long total = 0, x = 0, y = 0;
+    each([&](int i) { total += mass(i); });
+    reduce(total, x, y);
+    got = (double)total / UNIT;
     const double target = s.p * (sum >= 0.0 ? sum : got);
     if (!complete && got < target + slack) return CUT_SHORT;
-    const uint32_t d = digit_search<THREADS, KEY_BITS, false>(n, digits, mass, target * UNIT,
-                                                               sh.bucket, before, inside);
-    double w = 0.0;                                 // the weight of the tokens with digits d
-    int ties = 0;
+    const uint32_t d = digit_search<THREADS, false>(n, key_bits, digits, mass, target * UNIT,
+                                                    sh.bucket, before, inside);
+    // the tokens with digits d, and their weight
+    unsigned long long ties = 0, w_bits = 0;
+    x = 0;
     each([&](int i) {
-      if (is_kept(i) && digits(i) == d) { ++ties; w = weight_of(i); }
+      if (is_kept(i) && digits(i) == d) {
+        ++ties;
+        w_bits = (unsigned long long)__double_as_longlong(weight_of(i));
+      }
     });
-    ties = block_reduce<THREADS>(ties, sh.redi, OpAdd());
-    w = block_reduce<THREADS>(w, sh.red, OpMax());
-    const double ahead = (double)before / UNIT;
-    const int keep = ties_below(target, ahead, w, ties);
+    reduce(ties, x, w_bits);
+    const double w = __longlong_as_double((long long)w_bits), ahead = (double)before / UNIT;
+    const int keep = ties_below(target, ahead, w, (int)ties);
     if (slack > 0.0 && (target - (ahead + (keep - 1) * w) <= slack ||
                         ahead + keep * w - target <= slack))
       return CUT_AMBIGUOUS;
-    cut_at(d, keep, ties);
+    cut_at(d, keep, (int)ties);
   }
   if (s.mp > 0.0)
     each([&](int i) { if (weight_of(i) < s.mp) drop(i); });
-  if (s.p < 1.0 || s.mp > 0.0) total = total_mass();
-  // the last kept entry
-  unsigned long long last = 0;
-  int count = 0;
+  // the kept entries' sum, number and last one
+  unsigned long long total = 0, count = 0, last = 0;
   each([&](int i) {
-    if (is_kept(i)) { last = max(last, sh.list[i]); ++count; }
+    total += mass(i);
+    if (is_kept(i)) { ++count; last = max(last, sh.list[i]); }
   });
-  last = block_reduce<THREADS>(last, reinterpret_cast<unsigned long long*>(sh.red), OpMax());
-  count = block_reduce<THREADS>(count, sh.redi, OpAdd());
+  reduce(total, count, last);
   f.inv_sum = UNIT / (double)total;
   f.min_kept = key_logit(~(uint32_t)(last >> 32));
   f.last = (int)(uint32_t)last;
-  f.n_kept = count;
+  f.n_kept = (int)count;
   if (draw) {
-    const uint32_t t = digit_search<THREADS, 19, true>(n, id, mass, (double)u * (double)total,
-                                                       sh.bucket, before, inside);
+    const uint32_t t = digit_search<THREADS, true>(n, id_bits, id, mass,
+                                                   (double)u * (double)total, sh.bucket, before,
+                                                   inside);
     if (threadIdx.x == 0) sh.token = (int)t;
     __syncthreads();
   }
@@ -914,10 +976,10 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
     const unsigned long long e1 = l + kWave < n ? sh.list[l + kWave] : ~0ull;
     int r0 = 0, r1 = 0;
     if (n <= kWave) {
-#pragma unroll 8
+#pragma unroll 4
       for (int j = 0; j < n; ++j) r0 += sh.list[j] < e0;
     } else {
-#pragma unroll 8
+#pragma unroll 4
       for (int j = 0; j < n; ++j) {
         const unsigned long long y = sh.list[j];
         r0 += y < e0;
@@ -973,7 +1035,7 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
         if (draw) {
           // the kept entries by index
           int q0 = 0, q1 = 0;
-#pragma unroll 8
+#pragma unroll 4
           for (int j = 0; j < keep; ++j) {
             const uint32_t y = (uint32_t)so.entry[j];
             q0 += y < (uint32_t)e[0];
@@ -1027,7 +1089,7 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
                                                 sv_filter_row& f, int& count) {
   const int G = group_octets(V);
   const int tiles = (V + kRowTile - 1) / kRowTile;
-  const int groups = tiles * (8 / G) * kWave;
+  const int groups = tiles * (kRowTile / 8) / G;
   const bool by_k = s.k < V;
   const bool all = V <= kCand;                      // every token fits the list
   const bool need_sum = row_needs_sum(s, V);
@@ -1039,13 +1101,11 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
 #pragma unroll 1
   for (bool exact = PRE || !nucleus;; exact = true) {
     float top = -INFINITY;
-    uint32_t low = 0xffffffffu;
-    if constexpr (PRE) load_streamed<THREADS>(A, r, groups, tiles, need_sum, gm, sh, top, low);
-    else if (!need_sum) stream_row<LT, THREADS, NO_SUM>(row, V, s.c, G, gm, sh, top, low);
-    else if (exact) stream_row<LT, THREADS, SUM_F64>(row, V, s.c, G, gm, sh, top, low);
-    else stream_row<LT, THREADS, SUM_F32>(row, V, s.c, G, gm, sh, top, low);
+    if constexpr (PRE) load_streamed<THREADS>(A, r, groups, tiles, need_sum, gm, sh, top);
+    else if (!need_sum) stream_row<LT, THREADS, NO_SUM>(row, V, s.c, G, gm, sh, top);
+    else if (exact) stream_row<LT, THREADS, SUM_F64>(row, V, s.c, G, gm, sh, top);
+    else stream_row<LT, THREADS, SUM_F32>(row, V, s.c, G, gm, sh, top);
     const float m = block_reduce<THREADS>(top, reinterpret_cast<float*>(sh.redi), OpMax());
-    low = block_reduce<THREADS>(low, reinterpret_cast<uint32_t*>(sh.redi), OpMin());
     f = sv_filter_row{s.c, 0.0, m, INFINITY, -1, 0};
     if (m == -INFINITY) { count = 0; return true; }
     double S = -1.0;                                // the sum of all weights
@@ -1080,6 +1140,7 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
       mp_key = max(mp_key, min(kmax, logit_key(clean_logit(z)) - 2));
     }
     bool complete = true;                           // the list holds every kept token
+    bool first = false;
     double got = 0.0;
     uint32_t kt = kKeyNegInf + 1;
     ListCut cut = CUT_SHORT;
@@ -1087,18 +1148,20 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
     for (int attempt = 0; attempt < 8; ++attempt) {
       if (!all) {
         if (by_k || nucleus) {
-          // A nucleus row starts with the tokens of its kFirst largest groups,
-          // whose weights are then known exactly (two of the largest may share
-          // a group); what they lack of the share p, and a tenth more, is
-          // estimated from the group maxima below.
-          const bool est = nucleus && attempt > 0;
-          const int k = est ? 0 : nucleus ? min(kFirst, groups) : s.k;
-          const float z0 = est ? key_logit(kt) : m;
-          const float aim =
-              est ? (float)(1.1 * (s.p * S - got) / weight(z0, m, s.c, sh.table)) : 0.f;
+          // A nucleus row's share p of the sum is estimated from the group
+          // maxima; what the tokens found lack of it, and a tenth more, from
+          // those below.  Heavy tokens behind heavier ones of their group are
+          // missing from the first estimate: where it gave too many tokens,
+          // those of the kFirst largest groups come first.
+          const bool est = nucleus && !first, more = est && got > 0.0;
+          const int k = nucleus ? (est ? 0 : min(kFirst, groups)) : s.k;
+          const float z0 = more ? key_logit(kt) : m;
+          const double lack = more ? 1.1 * (s.p * S - got) : s.p * S;
+          const float aim = est ? (float)(lack / weight(z0, m, s.c, sh.table)) : 0.f;
           kt = s.k == 1 ? kmax
-                        : threshold_key<THREADS>(gm, groups, est ? kt - 1 : kmax, low,
-                                                 est ? uniform(sh.nq) : 0, z0, (float)s.c, k, aim, sh);
+                        : threshold_key<THREADS>(gm, groups, more ? kt - 1 : kmax,
+                                                 more ? uniform(sh.nq) : 0, z0, (float)s.c, k, aim,
+                                                 sh);
           complete = !nucleus || kt <= mp_key;
           if (nucleus || s.p >= 1.0) kt = max(kt, mp_key);
         } else {
@@ -1106,11 +1169,16 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
         }
       }
       const int n = gather_tokens<LT, THREADS>(row, V, G, groups, gm, key_logit(kt), sh);
-      if (n < 0) return false;
+      if (n < 0) {
+        if (!nucleus || attempt > 0) return false;
+        first = true;
+        continue;
+      }
+      first = false;
       count = n;
       cut = n <= kWaveList
                 ? cut_short_list<THREADS>(sh, n, s, m, S, slack, complete, draw, u, f, got)
-                : cut_list<LT, THREADS>(sh, n, s, V, m, S, slack, complete, draw, u, f, got);
+                : cut_list<LT, THREADS>(sh, n, s, V, m, kt, S, slack, complete, draw, u, f, got);
       if (cut != CUT_SHORT) break;
     }
     if (cut == CUT_SHORT) return false;
@@ -1220,13 +1288,25 @@ __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLau
   }
   const int t = blockIdx.y * (kStreamThreads / kWave) + threadIdx.x / kWave;
   if (t >= tiles) return;
-  float* gm = A.group_max + r * ((long)tiles * (8 / G) * kWave);
+  float* gm = A.group_max + r * ((long)tiles * (kRowTile / 8) / G);
   float* tm = A.tile_max + r * tiles + t;
   double* ts = A.tile_sum + r * tiles + t;
   float top = -INFINITY;
-  uint32_t low = 0xffffffffu;
-  if (sum) stream_tile<LT, SUM_F64>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
-  else stream_tile<LT, NO_SUM>(row, V, t, s.c, G, gm, tm, ts, table, top, low);
+  if (sum) stream_tile<LT, SUM_F64>(row, V, t, s.c, G, gm, tm, ts, table, top);
+  else stream_tile<LT, NO_SUM>(row, V, t, s.c, G, gm, tm, ts, table, top);
+}
+
+// Sets up a workgroup's LDS: RowShared, the list of `cap` entries, the group
+// maxima (returned).
+template <int THREADS>
+__device__ __forceinline__ float* row_shared(unsigned char* lds, int cap, RowShared<THREADS>& sh) {
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(lds + sizeof(RowShared<THREADS>));
+  fill_exp_table(sh.table, threadIdx.x, THREADS);
+  if (threadIdx.x == 0) {
+    sh.list = list;
+    sh.cap = cap;
+  }
+  return reinterpret_cast<float*>(list + cap);
 }
 
 // A row by the general path: the kept set by radix searches over the whole row,
@@ -1262,7 +1342,6 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4))) vo
 filter_rows_kernel(FilterLaunch A) {
   extern __shared__ __align__(16) unsigned char lds[];
   RowShared<THREADS>& sh = *reinterpret_cast<RowShared<THREADS>*>(lds);
-  float* gm = reinterpret_cast<float*>(lds + sizeof(RowShared<THREADS>));
   const long r = blockIdx.x;
   const int b = (int)(r / A.per_seq);
   const int V = A.V;
@@ -1275,7 +1354,7 @@ filter_rows_kernel(FilterLaunch A) {
   const LT* row = static_cast<const LT*>(A.logits) + (there ? ri : 0) * A.row_stride;
   const bool sampled = A.out_tokens && s.c != 0.0;
   const float u = sampled ? A.uniforms[r] : 0.f;
-  fill_exp_table(sh.table, threadIdx.x, THREADS);
+  float* gm = row_shared<THREADS>(lds, A.list_cap, sh);
   if (A.pending && r == 0 && threadIdx.x == 0) *A.pending = 0;
   __syncthreads();
   int count = 0;                                    // candidates in sh.list; -1: no list
@@ -1304,10 +1383,10 @@ filter_rows_kernel(FilterLaunch A) {
   if (threadIdx.x == 0) {
     if (errors) flag_error(A.device_error, errors);
     if (A.out_rows) A.out_rows[r] = f;
-    A.list_counts[r] = count;
+    A.list_counts[r] = count <= kCand ? count : -1;
     if (A.out_tokens) A.out_tokens[r] = token;
   }
-  if (A.lists)
+  if (A.lists && count <= kCand)
     for (int i = threadIdx.x; i < count; i += THREADS)
       A.lists[r * kCand + i] = (int32_t)(uint32_t)sh.list[i];
   if (A.out_probs) {
@@ -1392,7 +1471,7 @@ struct DrafterQ {
 template <typename LT, bool QL>
 __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(FilteredVerifyLaunch A) {
   __shared__ double red[kVerifyThreads / kWave];
-  __shared__ unsigned long long bucket[256];
+  __shared__ unsigned long long bucket[kBuckets];
   __shared__ double mass[kCand];
   __shared__ int id[kCand];
   __shared__ int sh_a;
@@ -1481,8 +1560,8 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
     });
     total = block_reduce<kVerifyThreads>(total, reinterpret_cast<unsigned long long*>(red), OpAdd());
     __syncthreads();
-    token = (int)digit_search<kVerifyThreads, 19, true>(
-        count, [&](int i) { return (uint32_t)id[i]; },
+    token = (int)digit_search<kVerifyThreads, true>(
+        count, bits_of((uint32_t)(V - 1)), [&](int i) { return (uint32_t)id[i]; },
         [&](int i) { return (unsigned long long)__double_as_longlong(mass[i]); },
         (double)u * (double)total, bucket, before, inside);
   }
@@ -1615,7 +1694,7 @@ struct FilterWorkspace {
       part(tile_mass, n * 2 * tiles * sizeof(double));
     }
     if (streams_apart(n, V)) {
-      part(group_max, n * tiles * (8 / group_octets(V)) * kWave * sizeof(float));
+      part(group_max, n * tiles * (kRowTile / 8) / group_octets(V) * sizeof(float));
       part(tile_max, n * tiles * sizeof(float));
       part(tile_sum, n * tiles * sizeof(double));
     }
@@ -1623,12 +1702,24 @@ struct FilterWorkspace {
   }
 };
 
+// LDS of a workgroup with a list of `cap`; the longest list in 64 KB, up to
+// kCandFew (enough for kCand at every V).
+template <int THREADS>
+size_t row_lds(int V, int cap) {
+  const int tiles = (V + kRowTile - 1) / kRowTile;
+  return sizeof(RowShared<THREADS>) + cap * sizeof(unsigned long long) +
+         (size_t)tiles * (kRowTile / 8) / group_octets(V) * sizeof(float);
+}
+template <int THREADS>
+int list_cap(int V) {
+  return row_lds<THREADS>(V, kCandFew) <= 65536 ? kCandFew : kCand;
+}
+
 template <typename LT, int THREADS, bool PRE, bool GENERAL>
-void launch_rows(const FilterLaunch& L, hipStream_t stream) {
-  const int tiles = (L.V + kRowTile - 1) / kRowTile;
-  const size_t gm = (size_t)tiles * (8 / group_octets(L.V)) * kWave * sizeof(float);
-  const size_t lds =
-      std::max(sizeof(RowShared<THREADS>) + gm, GENERAL ? sizeof(FilterShared<THREADS>) : 0);
+void launch_rows(FilterLaunch L, hipStream_t stream) {
+  L.list_cap = THREADS > 256 ? list_cap<THREADS>(L.V) : kCand;
+  const size_t lds = std::max(row_lds<THREADS>(L.V, L.list_cap),
+                              GENERAL ? sizeof(FilterShared<THREADS>) : 0);
   filter_rows_kernel<LT, THREADS, PRE, GENERAL>
       <<<dim3((unsigned)((long)L.B * L.per_seq)), THREADS, lds, stream>>>(L);
 }
