@@ -175,11 +175,56 @@ __device__ __forceinline__ T uniform(T x) {
   return x;
 }
 
-// Each gives every thread the result; sm holds one entry per wave.
+// x of the lane that a DPP control names, `old` in lanes without one.
+template <int CTRL, int ROWS = 0xf, typename T>
+__device__ __forceinline__ T dpp(T x, T old) {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one or two registers");
+  int w[sizeof(T) / 4], o[sizeof(T) / 4];
+  __builtin_memcpy(w, &x, sizeof(T));
+  __builtin_memcpy(o, &old, sizeof(T));
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) / 4; ++i)
+    w[i] = __builtin_amdgcn_update_dpp(o[i], w[i], CTRL, ROWS, 0xf, false);
+  __builtin_memcpy(&x, w, sizeof(T));
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ T of_lane(T x, int lane) {
+  int w[sizeof(T) / 4];
+  __builtin_memcpy(w, &x, sizeof(T));
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) / 4; ++i) w[i] = __builtin_amdgcn_readlane(w[i], lane);
+  __builtin_memcpy(&x, w, sizeof(T));
+  return x;
+}
+// Over a wave: rotations within its rows of 16 lanes, then the four rows'
+// results by readlane.  A step is a few instructions, where a shuffle through
+// LDS takes over 100 cycles.  The result is uniform.
+template <typename T, typename OP>
+__device__ __forceinline__ T wave_reduce(T x, OP op) {
+  x = op(x, dpp<0x128>(x, x));          // row_ror 8, 4, 2, 1
+  x = op(x, dpp<0x124>(x, x));
+  x = op(x, dpp<0x122>(x, x));
+  x = op(x, dpp<0x121>(x, x));
+  return op(op(of_lane(x, 0), of_lane(x, 16)), op(of_lane(x, 32), of_lane(x, 48)));
+}
+// Inclusive running totals over a wave's lanes: shifts within the rows, then
+// the last lanes of row 0 and 2 to the next rows, and of row 1 to the upper half.
+template <typename T>
+__device__ __forceinline__ T wave_prefix(T x) {
+  x += dpp<0x111>(x, T(0));             // row_shr 1, 2, 4, 8
+  x += dpp<0x112>(x, T(0));
+  x += dpp<0x114>(x, T(0));
+  x += dpp<0x118>(x, T(0));
+  x += dpp<0x142, 0xa>(x, T(0));        // row_bcast 15
+  x += dpp<0x143, 0xc>(x, T(0));        // row_bcast 31
+  return x;
+}
+
+// Over the workgroup; sm holds one entry per wave.
 template <int THREADS, typename T, typename OP>
 __device__ __forceinline__ T block_reduce(T x, T* sm, OP op) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) x = op(x, __shfl_xor(x, off));
+  x = wave_reduce(x, op);
   __syncthreads();                      // sm may still be read from before
   if (lane_id() == 0) sm[threadIdx.x / kWave] = x;
   __syncthreads();

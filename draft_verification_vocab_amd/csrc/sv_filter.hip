@@ -382,7 +382,7 @@ struct RowShared {
 // Exclusive running totals over the workgroup's threads, and the total.
 template <int THREADS>
 __device__ __forceinline__ double block_scan(double x, double* sm, double& total) {
-  const double incl = wave_inclusive_scan(x);
+  const double incl = wave_prefix(x);
   __syncthreads();
   if (lane_id() == kWave - 1) sm[threadIdx.x / kWave] = incl;
   __syncthreads();
@@ -472,7 +472,7 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
     }
     top = fmaxf(top, mt);
     if constexpr (SUM != NO_SUM) {
-      mt = wave_max(mt);
+      mt = wave_reduce(mt, OpMax());
       double s = 0.0, s1 = 0.0;
       // Logits 500 octaves and more below the maximum (and -inf, NaN) count
       // 2^-500.  Where z c loses too much in fp64, or that floor cannot be told
@@ -518,7 +518,7 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
           if (e < V) s += weight(clean_logit(logit_at(row, e)), mt, c, table);
         }
       }
-      s = wave_sum(s + s1);
+      s = wave_reduce(s + s1, OpAdd());
       if (mt > ref) {
         sum *= ref > -INFINITY ? weight(ref, mt, c, table) : 0.0;
         ref = mt;
@@ -606,13 +606,7 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
       int n[PER], mine = 0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) { n[i] = sh.top.cnt[l * PER + i]; mine += n[i]; }
-      int run = mine;
-#pragma unroll
-      for (int off = 1; off < kWave; off <<= 1) {
-        const int y = __shfl_up(run, off);
-        if (l >= off) run += y;
-      }
-      run += above - mine;
+      int run = wave_prefix(mine) + above - mine;
       int hit = -1, before = 0;
       float fbefore = 0.f;
       if (!by_mass) {
@@ -638,13 +632,7 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
           r += n[i];
           fmine += f[i];
         }
-        float frun = fmine;
-#pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) {
-          const float y = __shfl_up(frun, off);
-          if (l >= off) frun += y;
-        }
-        frun += mass - fmine;
+        float frun = wave_prefix(fmine) + mass - fmine;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           if (hit < 0 && n[i] && frun + most[i] >= aim) {
@@ -694,17 +682,24 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
   __syncthreads();
   if (threadIdx.x == 0) { sh.nq = 0; sh.n = 0; }
   __syncthreads();
+  // each thread's groups are counted first, for one addition to the counter
+  int mine = 0;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < groups; i += THREADS)
-    if (gm[i] >= zt) {
-      const int q = atomicAdd(&sh.nq, 1);
-      if (q < kQueue) sh.queue[q] = (uint16_t)i;
-    }
+  for (int i = threadIdx.x; i < groups; i += THREADS) mine += gm[i] >= zt;
+  if (mine) {
+    int q = atomicAdd(&sh.nq, mine);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < groups; i += THREADS)
+      if (gm[i] >= zt) {
+        if (q < kQueue) sh.queue[q] = (uint16_t)i;
+        ++q;
+      }
+  }
   __syncthreads();
   const int nq = uniform(sh.nq);
   if (nq > kQueue) return -1;
-  // 64 bytes a thread at a time, to have their loads in flight together
-  constexpr int BATCH = 8 / sizeof(LT);
+  // two octets a thread at a time
+  constexpr int BATCH = 2;
   const int items = nq * G;
 #pragma unroll 1
   for (int i0 = threadIdx.x; i0 < items; i0 += BATCH * THREADS) {
@@ -717,18 +712,29 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
       if (e[p] + 8 <= V) raw8(row + e[p], raw[p]);
       else raw8_end(row, e[p], V, raw[p]);
     }
+    // likewise the tokens
+    uint32_t hits = 0;                              // bit 8 p + j
 #pragma unroll
     for (int p = 0; p < BATCH; ++p) {
-      if (i0 + p * THREADS >= items) break;
       float z[8];
       unpack(raw[p], z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = clean_logit(z[j]);
-        if (x >= zt) {
-          const int at = atomicAdd(&sh.n, 1);
-          if (at < sh.cap) sh.list[at] = order_entry(logit_key(x), e[p] + j);
-        }
+      for (int j = 0; j < 8; ++j)
+        hits |= (uint32_t)(clean_logit(z[j]) >= zt && i0 + p * THREADS < items) << (8 * p + j);
+    }
+    if (hits) {
+      int at = atomicAdd(&sh.n, (int)__popc(hits));
+#pragma unroll
+      for (int p = 0; p < BATCH; ++p) {
+        keep_raw(raw[p]);
+        float z[8];
+        unpack(raw[p], z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((hits >> (8 * p + j)) & 1u) {
+            if (at < sh.cap) sh.list[at] = order_entry(logit_key(clean_logit(z[j])), e[p] + j);
+            ++at;
+          }
       }
     }
   }
@@ -776,34 +782,23 @@ __device__ __forceinline__ uint32_t digit_search(int n, int bits, K key, X x, do
     const auto find = [&](unsigned long long x, unsigned long long& run) {
       // the first lane at whose x the total is over the target, else the last with any
       const unsigned long long hits = __ballot(x && !past && over(run + x)), any = __ballot(x != 0);
-      const int src = hits ? __ffsll((long long)hits) - 1 : any ? 63 - __clzll((long long)any) : 0;
+      const int src =
+          uniform(hits ? __ffsll((long long)hits) - 1 : any ? 63 - __clzll((long long)any) : 0);
       past = past || !hits;
-      run = uniform(__shfl(run, src));
+      run = of_lane(run, src);
       return src;
     };
     unsigned long long mine = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) mine += bucket[l * PER + i];
-    unsigned long long run = mine;
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const unsigned long long y = __shfl_up(run, off);
-      if (l >= off) run += y;
-    }
-    run += before - mine;
+    unsigned long long run = wave_prefix(mine) + before - mine;
     const int lane = find(mine, run);
     const unsigned long long x8 = l < PER ? bucket[lane * PER + l] : 0;
-    unsigned long long in = x8;
-#pragma unroll
-    for (int off = 1; off < PER; off <<= 1) {
-      const unsigned long long y = __shfl_up(in, off);
-      if (l >= off) in += y;
-    }
-    run += in - x8;
+    run += wave_prefix(x8) - x8;
     const int at = find(x8, run);
     prefix = prefix << now | (uint32_t)(lane * PER + at);
     before = run;
-    inside = uniform(__shfl(x8, at));
+    inside = of_lane(x8, at);
     __syncthreads();
     rest -= now;
   }
@@ -877,12 +872,9 @@ __device__ __forceinline__ ListCut cut_list(RowShared<THREADS>& sh, int n, const
   };
   // sum, sum and maximum over the workgroup, in one go
   const auto reduce = [&](unsigned long long& a, unsigned long long& b, unsigned long long& c) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      a += __shfl_xor(a, off);
-      b += __shfl_xor(b, off);
-      c = max(c, __shfl_xor(c, off));
-    }
+    a = wave_reduce(a, OpAdd());
+    b = wave_reduce(b, OpAdd());
+    c = wave_reduce(c, OpMax());
     unsigned long long* red = reinterpret_cast<unsigned long long*>(sh.red);
     __syncthreads();
     if (lane_id() == 0) {
@@ -998,8 +990,8 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
       e[i] = 2 * l + i < n ? so.entry[2 * l + i] : 0;
       w[i] = 2 * l + i < nk ? weight(key_logit(~(uint32_t)(e[i] >> 32)), m, s.c, sh.table) : 0.0;
     }
-    const double incl = wave_inclusive_scan(w[0] + w[1]);
-    const double total = __shfl(incl, kWave - 1);
+    const double incl = wave_prefix(w[0] + w[1]);
+    const double total = of_lane(incl, kWave - 1);
     const double run0 = incl - (w[0] + w[1]), run1 = run0 + w[0];
     const double target = s.p * (sum >= 0.0 ? sum : total);
     ListCut c = CUT_DONE;
@@ -1017,16 +1009,14 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
         keep += k[i];
         most += in && (s.p >= 1.0 || run < target + slack);
       }
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) keep += __shfl_xor(keep, off);
+      keep = wave_reduce(keep, OpAdd());
       if (slack > 0.0) {
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) most += __shfl_xor(most, off);
+        most = wave_reduce(most, OpAdd());
         if (most != keep) c = CUT_AMBIGUOUS;
       }
       if (c == CUT_DONE) {
         const double part = (k[0] ? w[0] : 0.0) + (k[1] ? w[1] : 0.0);
-        const double S = wave_sum(part);
+        const double S = wave_reduce(part, OpAdd());
         const unsigned long long last = so.entry[keep - 1];
         f.inv_sum = 1.0 / S;
         f.min_kept = key_logit(~(uint32_t)(last >> 32));
@@ -1047,17 +1037,14 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
           double x[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) x[i] = 2 * l + i < keep ? so.w[2 * l + i] : 0.0;
-          const double at = wave_inclusive_scan(x[0] + x[1]);
-          const double goal = (double)u * __shfl(at, kWave - 1);
+          const double at = wave_prefix(x[0] + x[1]);
+          const double goal = (double)u * of_lane(at, kWave - 1);
           const double before = at - (x[0] + x[1]);
           int first = INT32_MAX, any = -1;
           if (x[0] > 0.0) { any = 2 * l; if (before + x[0] > goal) first = 2 * l; }
           if (x[1] > 0.0) { any = 2 * l + 1; if (at > goal) first = min(first, 2 * l + 1); }
-#pragma unroll
-          for (int off = 32; off >= 1; off >>= 1) {
-            first = min(first, __shfl_xor(first, off));
-            any = max(any, __shfl_xor(any, off));
-          }
+          first = wave_reduce(first, OpMin());
+          any = wave_reduce(any, OpMax());
           if (l == 0) sh.token = so.id[first == INT32_MAX ? any : first];
         }
       }
@@ -1207,8 +1194,8 @@ __device__ __forceinline__ int find_tile(const double* mass, int tiles, float u,
     x[i] = l * PER + i < tiles ? mass[l * PER + i] : 0.0;
     mine += x[i];
   }
-  const double incl = wave_inclusive_scan(mine);
-  target = (double)u * __shfl(incl, kWave - 1);
+  const double incl = wave_prefix(mine);
+  target = (double)u * of_lane(incl, kWave - 1);
   double run = incl - mine, at = 0.0;
   int hit = -1, any = -1;
 #pragma unroll
