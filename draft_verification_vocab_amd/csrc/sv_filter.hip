@@ -330,19 +330,18 @@ __device__ __forceinline__ sv_filter_row filter_row(const LT* row, int V, const 
 // ---------------------------------------------------------------- one pass over a row
 // The logits are streamed once.  A wave takes tiles of 4096 elements, lane l
 // the octets u = 0..7 at 512 u + 8 l of a tile; G adjacent octets are a group,
-// whose maximum goes to LDS (V / (8 G) of them).  The group maxima are logits
-// of the row, so the k-th largest of them is a lower bound of its k-th largest
-// logit: only groups whose maximum reaches a threshold found among them
-// (candidate groups) can hold kept tokens, and only those are read again, one
-// or two lines of memory each.  Where a filter needs the row's whole sum (top-p
-// without top-k, no filter at all) the pass also leaves every tile's maximum
-// and sum of weights.
+// whose largest logit's key, its upper 16 bits, goes to LDS (V / (8 G) of
+// them).  At least k logits reach the k-th largest of these, so only groups that
+// reach a threshold found among them (candidate groups) can hold kept tokens,
+// and only those are read again.  Where a filter needs the row's whole sum
+// (top-p without top-k, no filter at all) the pass also leaves every tile's
+// maximum and sum of weights.
 constexpr int kRowTile = 4096;
 constexpr int kRowTiles = SV_MAX_V / kRowTile;
 constexpr int kCand = 2048;            // candidate tokens of a row's list in the workspace, and in
                                        // LDS where many rows are worked on
 constexpr int kCandFew = 4096;         // ... in LDS elsewhere
-constexpr int kQueue = 2048;           // candidate groups
+constexpr int kQueue = 4096;           // candidate groups
 constexpr int kBuckets = 512;          // of a digit search
 constexpr int kTopBins = 256;          // histogram of the group maxima
 constexpr int kFirst = 96;             // groups a nucleus row falls back to
@@ -350,11 +349,16 @@ constexpr int kGeneralRow = -2;        // list_counts: the row takes the general
 constexpr int kMaxListK = 1024;        // largest top-k taken through the candidate list
 constexpr int kWaveList = 128;         // most candidates that one wave cuts and draws from
 
-// Octets per group: 8, or fewer as long as there are at most 3200 groups.
-__host__ __device__ __forceinline__ int group_octets(int V) {
-  const int octs = (V + 7) / 8;
-  return octs <= 3200 ? 1 : octs <= 6400 ? 2 : octs <= 12800 ? 4 : 8;
+// Octets per group: 1, 2, 4 or 8, for at most `most` groups where that does.
+// Smaller groups cost LDS and spare reading again: a candidate comes with G
+// octets.
+int group_octets(int V, int most) {
+  int G = 1;
+  while (G < 8 && (V + 7) / 8 > most * G) G *= 2;
+  return G;
 }
+constexpr int kGroups = 5120;          // ... where many rows are worked on
+constexpr int kGroupsFew = 10240;      // ... elsewhere
 
 template <int THREADS>
 struct RowShared {
@@ -423,18 +427,17 @@ __device__ __forceinline__ float max_adjacent(float x) {
   return x;
 }
 
-// One wave's tile t of a row: its groups' maxima to gm (the row's), with a sum
+// One wave's tile t of a row: its groups' keys to gm (the row's), with a sum
 // its maximum and sum of weights to *tile_m, *tile_s.  Gives the lane's largest
 // logit.  128 bytes a lane are in flight:
 // a bf16 tile at once, an fp32 tile in two parts.
 template <typename LT, RowSum SUM>
-__device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double c, int G, float* gm,
+__device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double c, int G, uint16_t* gm,
                                             float* tile_m, double* tile_s, const double* table,
                                             float& top) {
   constexpr int OCTS = 16 / sizeof(LT);
   const int l = lane_id();
   float ref = -INFINITY;                            // the sum's reference logit
-  float mine = -INFINITY;                           // G = 8: the maximum of octet l & 7's group
   double sum = 0.0;
 #pragma unroll 1
   for (int part = 0; part < 8 / OCTS; ++part) {
@@ -460,15 +463,13 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
                       fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
       g = clean_logit(g);
       mt = fmaxf(mt, g);
-      if (G == 8) {                                 // uniform
-        g = max_adjacent<8>(g);
-        mine = (l & 7) == part * OCTS + u ? g : mine;
-      } else {
-        if (G >= 2) g = max_adjacent<2>(g);
-        if (G >= 4) g = max_adjacent<4>(g);
-        if ((l & (G - 1)) == 0)
-          gm[(t * (kRowTile / 8) + (part * OCTS + u) * kWave + l) / G] = g;
-      }
+      // G is uniform
+      if (G == 8) g = max_adjacent<8>(g);
+      else if (G >= 2) g = max_adjacent<2>(g);
+      if (G == 4) g = max_adjacent<4>(g);
+      if ((l & (G - 1)) == 0)
+        gm[(t * (kRowTile / 8) + (part * OCTS + u) * kWave + l) / G] =
+            (uint16_t)(logit_key(g) >> 16);
     }
     top = fmaxf(top, mt);
     if constexpr (SUM != NO_SUM) {
@@ -526,14 +527,13 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
       if (mt > -INFINITY) sum += s * weight(mt, ref, c, table);
     }
   }
-  if (G == 8) gm[t * kWave + (l & 7) * 8 + (l >> 3)] = mine;
   if constexpr (SUM != NO_SUM)
     if (l == 0) { *tile_m = ref; *tile_s = sum; }
 }
 
 // A whole row by one workgroup, into LDS.
 template <typename LT, int THREADS, RowSum SUM>
-__device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G, float* gm,
+__device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G, uint16_t* gm,
                                            RowShared<THREADS>& sh, float& top) {
   const int tiles = (V + kRowTile - 1) / kRowTile;
   for (int t = threadIdx.x / kWave; t < tiles; t += THREADS / kWave)
@@ -543,14 +543,12 @@ __device__ __forceinline__ void stream_row(const LT* row, int V, double c, int G
 // What a row's stream leaves, where a kernel of its own made it: into LDS.
 template <int THREADS>
 __device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int groups, int tiles,
-                                              bool sum, float* gm, RowShared<THREADS>& sh,
+                                              bool sum, uint16_t* gm, RowShared<THREADS>& sh,
                                               float& top) {
-  const float* g = A.group_max + r * groups;
-  for (int i = threadIdx.x; i < groups; i += THREADS) {
-    const float x = g[i];
-    gm[i] = x;
-    top = fmaxf(top, x);
-  }
+  // groups is even: a pair of keys at a time
+  const uint32_t* g = reinterpret_cast<const uint32_t*>(A.group_key + r * groups);
+  for (int i = threadIdx.x; i < groups / 2; i += THREADS) reinterpret_cast<uint32_t*>(gm)[i] = g[i];
+  for (int t = threadIdx.x; t < tiles; t += THREADS) top = fmaxf(top, A.tile_max[r * tiles + t]);
   if (sum)
     for (int t = threadIdx.x; t < tiles; t += THREADS) {
       sh.tile_m[t] = A.tile_max[r * tiles + t];
@@ -558,45 +556,45 @@ __device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int
     }
 }
 
-// The key from which on logits can be kept, from the group maxima: at least k
-// of them reach it (by count, k > 0), or the weights of the logits that do are
-// about `aim` times that of logit z0 (by mass, k = 0).  Histograms of the maxima's keys, the first
-// over their whole range, then over the bin of the threshold while that bin is
-// wide.  A maximum stands for the group's tokens of its own size; in the
+// The key (its upper 16 bits) from which on logits can be kept, from the
+// groups' keys: at least k of them reach it (by count, k > 0), or the weights of
+// the logits that do are about `aim` times that of logit z0 (by mass, k = 0).
+// One histogram of the 256 keys from `hi` down, two binades; where that does not
+// reach, one of all keys below and, if the threshold's bin is crowded, of that
+// bin.  A group's largest logit stands for its tokens of that size; in the
 // estimate of the mass, those hidden behind a larger one of their group are
-// added as 1 / (share of groups without a larger one).  The search starts at
-// key `hi`, `above` groups lying above it; the lowest finite key if nothing
-// reaches it.
-template <int THREADS>
-__device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, uint32_t hi,
+// added from the share of groups without a larger one.  `above` groups lie above
+// `hi`.  The lowest finite key if nothing reaches it.
+constexpr uint32_t kLowest = (kKeyNegInf + 1) >> 16;
+template <typename LT, int THREADS>
+__device__ __forceinline__ uint32_t threshold_key(const uint16_t* gm, int groups, uint32_t hi,
                                                   int above, float z0, float c, int k,
                                                   float aim, RowShared<THREADS>& sh) {
   const bool by_mass = k == 0;
-  constexpr uint32_t FLOOR = kKeyNegInf + 1;
-  if (hi < FLOOR) return FLOOR;
+  if (hi < kLowest) return kLowest;
   float mass = 0.f;                    // estimated mass found
-  // a binade first: the threshold of a row's largest logits is mostly there, in
-  // narrow bins
-  bool near = hi - FLOOR > 0x800000u;
-  uint32_t lo = near ? hi - 0x800000u : FLOOR;
+  bool near = hi - kLowest >= kTopBins;
+  uint32_t lo = near ? hi - (kTopBins - 1) : kLowest;
 #pragma unroll 1
-  for (int level = 0; level < 5; ++level) {
-    // hi - lo < 256 << shift
-    const int shift = max(0, 24 - __clz((int)(hi - lo | 1u)));
+  for (int level = 0; level < 3; ++level) {
+    const int shift = hi - lo < kTopBins ? 0 : 8;
     __syncthreads();
     for (int i = threadIdx.x; i < kTopBins; i += THREADS) sh.top.cnt[i] = sh.top.mass[i] = 0;
     if (threadIdx.x == 0) sh.bin = -1;
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < groups; i += THREADS) {
-      const float g = gm[i];
-      const uint32_t key = logit_key(g);
+      const uint32_t key = gm[i];
       if (key <= hi && key >= lo) {
         const uint32_t b = (hi - key) >> shift;
         atomicAdd(&sh.top.cnt[b], 1u);
-        if (by_mass)
+        if (by_mass) {
+          // the logit: exactly (bf16), or the middle of those with this half of a key
+          const float g = key_logit(key << 16 | (sizeof(LT) == 4 ? 0x8000u
+                                                 : key & 0x8000u ? 0u : 0xffffu));
           atomicAdd(&sh.top.mass[b],
                     g >= z0 ? 262144u : (uint32_t)(__builtin_amdgcn_exp2f((g - z0) * c) * 262144.f));
+        }
       }
     }
     __syncthreads();
@@ -650,47 +648,56 @@ __device__ __forceinline__ uint32_t threshold_key(const float* gm, int groups, u
     __syncthreads();
     const int b = uniform(sh.bin);
     if (b < 0) {
-      if (near) {                                   // not within the binade
+      if (near) {
         near = false;
-        lo = FLOOR;
+        lo = kLowest;
         continue;
       }
       // not reached: every token, or (by mass, inside a bin that seemed to
       // reach it) what there is
       return lo;
     }
+    if (shift == 0) return hi - b;
     near = false;
     above = uniform(sh.above);
     mass = uniform(sh.frac);
     const int in = (int)uniform(sh.top.cnt[b]);
     const uint32_t top = hi - ((uint32_t)b << shift);
-    const uint32_t width = (1u << shift) - 1;
-    const uint32_t bottom = top - lo > width ? top - width : lo;
-    if (in <= above / 4 + 32 || shift == 0) return bottom;
+    const uint32_t bottom = top - lo > 255 ? top - 255 : lo;
+    if (in <= above / 4 + 32) return bottom;
     hi = top;
     lo = bottom;
   }
   return lo;
 }
 
-// The tokens whose logit is at least zt into sh.list, in any order.  Returns their number, or -1 if they or their groups
+// The tokens whose key is at least kt into sh.list, in any order.  Returns their number, or -1 if they or their groups
 // are more than the lists hold.
 template <typename LT, int THREADS>
 __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int groups,
-                                             const float* gm, float zt,
+                                             const uint16_t* gm, uint32_t kt,
                                              RowShared<THREADS>& sh) {
+  const float zt = key_logit(kt);
+  const uint32_t kg = kt >> 16;
   __syncthreads();
   if (threadIdx.x == 0) { sh.nq = 0; sh.n = 0; }
   __syncthreads();
-  // each thread's groups are counted first, for one addition to the counter
+  // Places for each lane's c entries, by one addition per wave: of its own, the
+  // compiler would add up the lanes of a divergent addition one after the other.
+  const auto place = [](int* counter, int c) {
+    const int incl = wave_prefix(c), all = of_lane(incl, kWave - 1);
+    int base = 0;
+    if (all && lane_id() == 0) base = atomicAdd(counter, all);
+    return uniform(base) + incl - c;
+  };
   int mine = 0;
-#pragma unroll 1
-  for (int i = threadIdx.x; i < groups; i += THREADS) mine += gm[i] >= zt;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < groups; i += THREADS) mine += gm[i] >= kg;
+  int q = place(&sh.nq, mine);
   if (mine) {
-    int q = atomicAdd(&sh.nq, mine);
-#pragma unroll 1
+#pragma unroll 4
     for (int i = threadIdx.x; i < groups; i += THREADS)
-      if (gm[i] >= zt) {
+      if (gm[i] >= kg) {
         if (q < kQueue) sh.queue[q] = (uint16_t)i;
         ++q;
       }
@@ -702,7 +709,8 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
   constexpr int BATCH = 2;
   const int items = nq * G;
 #pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < items; i0 += BATCH * THREADS) {
+  for (int base = 0; base < items; base += BATCH * THREADS) {
+    const int i0 = base + threadIdx.x;
     Raw<LT> raw[BATCH];
     int e[BATCH];
 #pragma unroll
@@ -712,7 +720,6 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
       if (e[p] + 8 <= V) raw8(row + e[p], raw[p]);
       else raw8_end(row, e[p], V, raw[p]);
     }
-    // likewise the tokens
     uint32_t hits = 0;                              // bit 8 p + j
 #pragma unroll
     for (int p = 0; p < BATCH; ++p) {
@@ -722,8 +729,8 @@ __device__ __forceinline__ int gather_tokens(const LT* row, int V, int G, int gr
       for (int j = 0; j < 8; ++j)
         hits |= (uint32_t)(clean_logit(z[j]) >= zt && i0 + p * THREADS < items) << (8 * p + j);
     }
+    int at = place(&sh.n, (int)__popc(hits));
     if (hits) {
-      int at = atomicAdd(&sh.n, (int)__popc(hits));
 #pragma unroll
       for (int p = 0; p < BATCH; ++p) {
         keep_raw(raw[p]);
@@ -1072,9 +1079,9 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
 template <typename LT, int THREADS, bool PRE>
 __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, const LT* row, int V,
                                                 const FilterSettings& s, bool draw, float u,
-                                                float* gm, RowShared<THREADS>& sh,
+                                                uint16_t* gm, RowShared<THREADS>& sh,
                                                 sv_filter_row& f, int& count) {
-  const int G = group_octets(V);
+  const int G = A.group_octets;
   const int tiles = (V + kRowTile - 1) / kRowTile;
   const int groups = tiles * (kRowTile / 8) / G;
   const bool by_k = s.k < V;
@@ -1145,17 +1152,18 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
           const float z0 = more ? key_logit(kt) : m;
           const double lack = more ? 1.1 * (s.p * S - got) : s.p * S;
           const float aim = est ? (float)(lack / weight(z0, m, s.c, sh.table)) : 0.f;
-          kt = s.k == 1 ? kmax
-                        : threshold_key<THREADS>(gm, groups, more ? kt - 1 : kmax,
-                                                 more ? uniform(sh.nq) : 0, z0, (float)s.c, k, aim,
-                                                 sh);
+          kt = (s.k == 1 ? kmax >> 16
+                         : threshold_key<LT, THREADS>(
+                               gm, groups, (more ? kt : kmax + 0x10000u) / 0x10000u - 1,
+                               more ? uniform(sh.nq) : 0, z0, (float)s.c, k, aim, sh))
+               << 16;
           complete = !nucleus || kt <= mp_key;
           if (nucleus || s.p >= 1.0) kt = max(kt, mp_key);
         } else {
           kt = mp_key;
         }
       }
-      const int n = gather_tokens<LT, THREADS>(row, V, G, groups, gm, key_logit(kt), sh);
+      const int n = gather_tokens<LT, THREADS>(row, V, G, groups, gm, kt, sh);
       if (n < 0) {
         if (!nucleus || attempt > 0) return false;
         first = true;
@@ -1260,7 +1268,7 @@ template <typename LT>
 __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLaunch A) {
   __shared__ double table[kExpTable];
   const long r = blockIdx.x;
-  const int V = A.V, G = group_octets(V);
+  const int V = A.V, G = A.group_octets;
   const int tiles = (V + kRowTile - 1) / kRowTile;
   int errors = 0;
   const FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps,
@@ -1275,25 +1283,27 @@ __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLau
   }
   const int t = blockIdx.y * (kStreamThreads / kWave) + threadIdx.x / kWave;
   if (t >= tiles) return;
-  float* gm = A.group_max + r * ((long)tiles * (kRowTile / 8) / G);
+  uint16_t* gm = A.group_key + r * ((long)tiles * (kRowTile / 8) / G);
   float* tm = A.tile_max + r * tiles + t;
   double* ts = A.tile_sum + r * tiles + t;
   float top = -INFINITY;
   if (sum) stream_tile<LT, SUM_F64>(row, V, t, s.c, G, gm, tm, ts, table, top);
   else stream_tile<LT, NO_SUM>(row, V, t, s.c, G, gm, tm, ts, table, top);
+  top = wave_reduce(top, OpMax());
+  if (lane_id() == 0) *tm = top;
 }
 
-// Sets up a workgroup's LDS: RowShared, the list of `cap` entries, the group
-// maxima (returned).
+// Sets up a workgroup's LDS: RowShared, the list of `cap` entries, the groups'
+// keys (returned).
 template <int THREADS>
-__device__ __forceinline__ float* row_shared(unsigned char* lds, int cap, RowShared<THREADS>& sh) {
+__device__ __forceinline__ uint16_t* row_shared(unsigned char* lds, int cap, RowShared<THREADS>& sh) {
   unsigned long long* list = reinterpret_cast<unsigned long long*>(lds + sizeof(RowShared<THREADS>));
   fill_exp_table(sh.table, threadIdx.x, THREADS);
   if (threadIdx.x == 0) {
     sh.list = list;
     sh.cap = cap;
   }
-  return reinterpret_cast<float*>(list + cap);
+  return reinterpret_cast<uint16_t*>(list + cap);
 }
 
 // A row by the general path: the kept set by radix searches over the whole row,
@@ -1341,7 +1351,7 @@ filter_rows_kernel(FilterLaunch A) {
   const LT* row = static_cast<const LT*>(A.logits) + (there ? ri : 0) * A.row_stride;
   const bool sampled = A.out_tokens && s.c != 0.0;
   const float u = sampled ? A.uniforms[r] : 0.f;
-  float* gm = row_shared<THREADS>(lds, A.list_cap, sh);
+  uint16_t* gm = row_shared<THREADS>(lds, A.list_cap, sh);
   if (A.pending && r == 0 && threadIdx.x == 0) *A.pending = 0;
   __syncthreads();
   int count = 0;                                    // candidates in sh.list; -1: no list
@@ -1663,7 +1673,7 @@ bool streams_apart(long rows, int V) { return few_rows(rows) && V > 16 * kRowTil
 // The parts of the workspace, in order; each starts at a multiple of 16 bytes.
 struct FilterWorkspace {
   size_t rows = 0, counts = 0, lists = 0, pending = 0, done = 0, tile_mass = 0;
-  size_t group_max = 0, tile_max = 0, tile_sum = 0, bytes = 0;
+  size_t group_key = 0, tile_max = 0, tile_sum = 0, bytes = 0;
   FilterWorkspace(long n, int V, bool verify) {
     const size_t tiles = (V + kRowTile - 1) / kRowTile;
     size_t at = 0;
@@ -1681,7 +1691,7 @@ struct FilterWorkspace {
       part(tile_mass, n * 2 * tiles * sizeof(double));
     }
     if (streams_apart(n, V)) {
-      part(group_max, n * tiles * (kRowTile / 8) / group_octets(V) * sizeof(float));
+      part(group_key, n * tiles * (kRowTile / 8) / group_octets(V, kGroupsFew) * sizeof(uint16_t));
       part(tile_max, n * tiles * sizeof(float));
       part(tile_sum, n * tiles * sizeof(double));
     }
@@ -1689,32 +1699,26 @@ struct FilterWorkspace {
   }
 };
 
-// LDS of a workgroup with a list of `cap`; the longest list in 64 KB, up to
-// kCandFew (enough for kCand at every V).
-template <int THREADS>
-size_t row_lds(int V, int cap) {
-  const int tiles = (V + kRowTile - 1) / kRowTile;
-  return sizeof(RowShared<THREADS>) + cap * sizeof(unsigned long long) +
-         (size_t)tiles * (kRowTile / 8) / group_octets(V) * sizeof(float);
-}
-template <int THREADS>
-int list_cap(int V) {
-  return row_lds<THREADS>(V, kCandFew) <= 65536 ? kCandFew : kCand;
-}
-
 template <typename LT, int THREADS, bool PRE, bool GENERAL>
 void launch_rows(FilterLaunch L, hipStream_t stream) {
-  L.list_cap = THREADS > 256 ? list_cap<THREADS>(L.V) : kCand;
-  const size_t lds = std::max(row_lds<THREADS>(L.V, L.list_cap),
+  const size_t tiles = (L.V + kRowTile - 1) / kRowTile;
+  const size_t keys = tiles * (kRowTile / 8) / L.group_octets * sizeof(uint16_t);
+  // few rows: as long a list as 64 KB of LDS hold
+  const size_t fixed = sizeof(RowShared<THREADS>) + keys;
+  L.list_cap = kCand;
+  if (few_rows((long)L.B * L.per_seq))
+    L.list_cap = (int)std::min((size_t)kCandFew, (65536 - fixed) / sizeof(unsigned long long));
+  const size_t lds = std::max(fixed + L.list_cap * sizeof(unsigned long long),
                               GENERAL ? sizeof(FilterShared<THREADS>) : 0);
   filter_rows_kernel<LT, THREADS, PRE, GENERAL>
       <<<dim3((unsigned)((long)L.B * L.per_seq)), THREADS, lds, stream>>>(L);
 }
 
 template <typename LT>
-hipError_t launch_filter(const FilterLaunch& L, hipStream_t stream) {
+hipError_t launch_filter(FilterLaunch L, hipStream_t stream) {
   const long rows = (long)L.B * L.per_seq;
   const int tiles = (L.V + kRowTile - 1) / kRowTile;
+  L.group_octets = group_octets(L.V, few_rows(rows) ? kGroupsFew : kGroups);
   if (streams_apart(rows, L.V)) {
     const int waves = kStreamThreads / kWave;
     trace_before(stream, SV_KERNEL_FILTER_ROWS);
@@ -1774,7 +1778,7 @@ hipError_t launch_filter_rows(const FilterLaunch& L0, hipStream_t stream) {
     L.pending = reinterpret_cast<int32_t*>(ws + at.pending);
   }
   L.list_counts = reinterpret_cast<int32_t*>(ws + at.counts);
-  L.group_max = reinterpret_cast<float*>(ws + at.group_max);
+  L.group_key = reinterpret_cast<uint16_t*>(ws + at.group_key);
   L.tile_max = reinterpret_cast<float*>(ws + at.tile_max);
   L.tile_sum = reinterpret_cast<double*>(ws + at.tile_sum);
   return L.bf16 ? launch_filter<uint16_t>(L, stream) : launch_filter<float>(L, stream);

@@ -124,9 +124,10 @@ struct FilterLaunch {
   // in the workspace, set by the launch
   int32_t* lists;                // kept tokens (and a few more), or NULL
   int32_t* list_counts;          // their number per row; -1: no list; -2: left to the general path
+  int group_octets;              // octets of a group
   int list_cap;                  // candidates a workgroup's list in LDS holds
   int32_t* pending;              // its counter is cleared here for the verify; or NULL
-  float* group_max;
+  uint16_t* group_key;
   float* tile_max;
   double* tile_sum;
 };
