@@ -1598,12 +1598,14 @@ __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerify
       z = clean_logit(z);
       return row_keeps(f, z, x) ? weight(z, f.max, f.scale, table) * f.inv_sum : 0.0;
     };
+    const auto q_of = [&](float z, int x) {          // from the drafter's logit
+      z = clean_logit(z);
+      return row_keeps(q.row, z, x) ? weight(z, q.row.max, q.row.scale, table) * q.row.inv_sum
+                                    : 0.0;
+    };
     const auto q_at = [&](int x) {
       if constexpr (QL) {
-        if (!q.logits) return 0.0;
-        const float z = clean_logit(logit_at(q.logits, x));
-        return row_keeps(q.row, z, x) ? weight(z, q.row.max, q.row.scale, table) * q.row.inv_sum
-                                      : 0.0;
+        return q.logits ? q_of(logit_at(q.logits, x), x) : 0.0;
       } else {
         return (double)q.probs[x];
       }
@@ -1615,17 +1617,52 @@ __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerify
     const int t = (int)(item % parts) * WAVES + w;
     if (t < tiles) {
       double rs = 0.0, ps = 0.0;
-#pragma unroll 4
-      for (int i = 0; i < kRowTile / kWave; ++i) {
-        const int x = t * kRowTile + i * kWave + l;
-        if (x < V) {
-          const double p = p_at(logit_at(za, x), x);
-          ps += p;
-          if (residual && p > 0.0) rs += fmax(0.0, p - q_at(x));
+      // two octets of the row and of q at a time
+#pragma unroll 1
+      for (int u = 0; u < 8; u += 2) {
+        Raw<LT> rz[2], rq[2];
+        float qf[2][8];
+        const int e0 = t * kRowTile + u * kTile + 8 * l;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int e = e0 + i * kTile;
+          if (e + 8 <= V) raw8(za + e, rz[i]);
+          else raw8_end(za, e, V, rz[i]);
+          if (residual) {
+            if constexpr (QL) {
+              if (q.logits) {
+                if (e + 8 <= V) raw8(q.logits + e, rq[i]);
+                else raw8_end(q.logits, e, V, rq[i]);
+              }
+            } else if (e + 8 <= V) {
+              load8(q.probs + e, qf[i]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) qf[i][j] = e + j < V ? q.probs[e + j] : 0.f;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int e = e0 + i * kTile;
+          float z[8], zq[8];
+          unpack(rz[i], z);
+          if constexpr (QL) unpack(rq[i], zq);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const double p = e + j < V ? p_at(z[j], e + j) : 0.0;
+            ps += p;
+            if (residual && p > 0.0) {
+              double x;
+              if constexpr (QL) x = q.logits ? q_of(zq[j], e + j) : 0.0;
+              else x = (double)qf[i][j];
+              rs += fmax(0.0, p - x);
+            }
+          }
         }
       }
-      rs = wave_sum(rs);
-      ps = wave_sum(ps);
+      rs = wave_reduce(rs, OpAdd());
+      ps = wave_reduce(ps, OpAdd());
       if (l == 0) {
         st_coherent(rmass + t, rs);
         st_coherent(pmass + t, ps);
