@@ -59,20 +59,18 @@ __device__ __forceinline__ double exp2_f64(double x) {
   return ldexp(p, (int)n);
 }
 
-// 2^x for -1000 <= x <= 0 with a table: x = k/512 + r with |r| <= 1/1024,
-// 2^(k/512) from the table (fp64, in LDS; its exponent raised by the whole part
-// of k/512) and 2^r = 1 + q(r).  Adding 1.5 * 2^43 rounds x to a multiple of
-// 1/512 and leaves k in the sum's low word.  With q = r (c1 + r c2), c1 and c2
-// chosen for the smallest largest error on that range, it is exact to 1.3e-11,
-// at about 13 instructions against more than 20 of exp2_f64, whose rounding and
-// scaling are of the slower kind (for the long sums); with the exponential
-// series up to r^3 (LONG) to 1e-14.
-constexpr int kExpTable = 512;
+// 2^x for -1000 <= x <= 0 with a table: x = k/64 + r with |r| <= 1/128, 2^(k/64)
+// from the table and 2^r by the exponential series up to r^5, exact to 1e-15.
+// Adding 1.5 * 2^46 rounds x to a multiple of 1/64 and leaves k in the sum's low
+// word.  The table is 64 doubles, two for each pair of LDS banks, so that lanes
+// reading different entries hardly wait for each other.  Entry j is kept less
+// j << 46: adding k << 14 to its high word puts in the whole part of k/64.
+constexpr int kExpTable = 64;
 struct ExpTable {
-  double v[kExpTable];
+  unsigned long long v[kExpTable];
   constexpr ExpTable() : v() {
     for (int i = 0; i < kExpTable; ++i) {
-      // 2^(i/512) as the square of the exponential series of half its logarithm
+      // 2^(i/64) as the square of the exponential series of half its logarithm
       const double y = 0.69314718055994530942 * i / (2.0 * kExpTable);
       double term = 1.0, sum = 0.0;
       for (int k = 24; k >= 0; --k) {               // smallest terms first
@@ -80,28 +78,45 @@ struct ExpTable {
         for (int j = 1; j <= k; ++j) term *= y / j;
         sum += term;
       }
-      v[i] = sum * sum;
+      v[i] = __builtin_bit_cast(unsigned long long, sum * sum) - ((unsigned long long)i << 46);
     }
   }
 };
 __device__ constexpr ExpTable kExp2Table;
-__device__ __forceinline__ void fill_exp_table(double* table, int t, int threads) {
-#pragma unroll 2
-  for (int i = t; i < kExpTable; i += threads) table[i] = kExp2Table.v[i];
+typedef unsigned long long ExpEntry;
+__device__ __forceinline__ void fill_exp_table(ExpEntry* table) {
+  if (threadIdx.x < kExpTable) table[threadIdx.x] = kExp2Table.v[threadIdx.x];
 }
-template <bool LONG>
-__device__ __forceinline__ double exp2_table(double x, const double* table) {
-  const double y = x + 0x1.8p43;
+constexpr double kExpRound = 0x1.8p46;
+// 2^(k/64), k the low word of kExpRound + k/64.
+__device__ __forceinline__ double table_entry(double y, const ExpEntry* table) {
   const uint32_t k = (uint32_t)__double_as_longlong(y);
-  const double r = x - (y - 0x1.8p43);
-  const unsigned long long t = __double_as_longlong(table[k & (kExpTable - 1)]);
-  const uint32_t hi = (uint32_t)(t >> 32) + ((k & ~(uint32_t)(kExpTable - 1)) << 11);
-  const double T = __longlong_as_double(((unsigned long long)hi << 32) | (uint32_t)t);
-  if constexpr (LONG)
-    return fma(T, r * fma(r, fma(r, 5.5504108664821580e-02, 2.4022650695910071e-01),
-                          6.9314718055994531e-01), T);
-  return fma(T, r * fma(r, 0.24022651860784677, 0.6931472202592015), T);
+  const ExpEntry t = table[k % kExpTable];
+  return __longlong_as_double((ExpEntry)((uint32_t)(t >> 32) + (k << 14)) << 32 | (uint32_t)t);
 }
+__device__ __forceinline__ double exp2_table(double x, const ExpEntry* table) {
+  const double y = x + kExpRound, r = x - (y - kExpRound);
+  const double T = table_entry(y, table);
+  const double q = fma(r, fma(r, fma(r, fma(r, 1.3333558146428443e-03, 9.6181291076284770e-03),
+                                     5.5504108664821580e-02), 2.4022650695910071e-01),
+                       6.9314718055994531e-01);
+  return fma(T, r * q, T);
+}
+// 2^r for the long sums: the series up to r^4 with r^4 replaced by the polynomial
+// h^2 r^2 - h^4/8 that comes nearest to it on |r| <= h = 1/128: exact to 5e-12.
+struct TwoTo {
+  // The coefficients are taken up where the object stands: hoisted out of the
+  // caller's outer loops they would take the registers that are short there.
+  double c[4] = {0.99999999999552125, 0.69314718055994529, 0.24022709400311362,
+                 0.055504108664821576};
+  __device__ __forceinline__ TwoTo() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+s"(c[i]));
+  }
+  __device__ __forceinline__ double operator()(double r) const {
+    return fma(r, fma(r, fma(r, c[3], c[2]), c[1]), c[0]);
+  }
+};
 
 // The weight of logit z in a row of maximum m: 1 at the maximum (also where
 // that is +inf), 0 at -inf.
@@ -111,10 +126,10 @@ __device__ __forceinline__ double weight(float z, float m, double c) {
 }
 
 // The same with a table, to 1e-14 (0 below 2^-1000).
-__device__ __forceinline__ double weight(float z, float m, double c, const double* table) {
+__device__ __forceinline__ double weight(float z, float m, double c, const ExpEntry* table) {
   if (z == m) return 1.0;
   const double x = ((double)z - (double)m) * c;
-  return z > -INFINITY && x > -1000.0 ? exp2_table<true>(x, table) : 0.0;
+  return z > -INFINITY && x > -1000.0 ? exp2_table(x, table) : 0.0;
 }
 
 // Whether a filter row keeps token x of logit z (cleaned).
@@ -131,8 +146,8 @@ __device__ __forceinline__ double row_prob(const sv_filter_row& f, float z, long
 struct FilterSettings {
   double c;      // log2(e) / T; 0: greedy
   int k;         // 1 .. V (V: off)
-  double p;      // >= 1: off
-  double mp;     // <= 0: off
+  float p;       // >= 1: off
+  float mp;      // <= 0: off
   bool off;      // no filter at all
 };
 
@@ -156,8 +171,8 @@ __device__ __forceinline__ FilterSettings filter_settings(const float* temperatu
   if (!(mp >= 0.f && mp <= 1.f)) { errors |= SV_DEVERR_FILTER; mp = 0.f; }
   if (c32 == 0.f) { k = 1; p = 1.f; mp = 0.f; }
   s.k = k == 0 || k > V ? V : k;
-  s.p = (double)p;
-  s.mp = (double)mp;
+  s.p = p;
+  s.mp = mp;
   s.off = s.k == V && s.p >= 1.0 && s.mp <= 0.0 && c32 != 0.f;
   return s;
 }

@@ -370,7 +370,7 @@ struct RowShared {
   };
   double tile_s[kRowTiles];
   float tile_m[kRowTiles];
-  double table[kExpTable];
+  ExpEntry table[kExpTable];
   double red[3 * (THREADS / kWave)];
   int redi[THREADS / kWave];
   unsigned long long* list;            // candidates: order_entry; cap of them at most
@@ -410,7 +410,10 @@ __device__ __forceinline__ unsigned long long order_entry(uint32_t key, int e) {
 __device__ __forceinline__ bool row_needs_sum(const FilterSettings& s, int V) {
   return V > kCand && s.k >= V && (s.p < 1.0 || s.off);
 }
-// How the stream takes it.
+
+// How the stream takes it.  By workgroups of rows SUM_F32 takes 0.6 of SUM_F64's
+// time for a nucleus row (650 against 1000 us for 7168 rows of 151936), and one row
+// in a hundred has to be streamed again for its cut.
 enum RowSum { NO_SUM, SUM_F32, SUM_F64 };
 
 // The maximum over N = 2, 4 or 8 adjacent lanes (from the maximum over N / 2,
@@ -433,10 +436,11 @@ __device__ __forceinline__ float max_adjacent(float x) {
 // a bf16 tile at once, an fp32 tile in two parts.
 template <typename LT, RowSum SUM>
 __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double c, int G, uint16_t* gm,
-                                            float* tile_m, double* tile_s, const double* table,
+                                            float* tile_m, double* tile_s, const ExpEntry* table,
                                             float& top) {
   constexpr int OCTS = 16 / sizeof(LT);
-  const int l = lane_id();
+  int l = lane_id();
+  asm volatile("" : "+v"(l));                       // its addresses are not kept past a tile
   float ref = -INFINITY;                            // the sum's reference logit
   double sum = 0.0;
 #pragma unroll 1
@@ -475,18 +479,14 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
     if constexpr (SUM != NO_SUM) {
       mt = wave_reduce(mt, OpMax());
       double s = 0.0, s1 = 0.0;
-      // Logits 500 octaves and more below the maximum (and -inf, NaN) count
-      // 2^-500.  Where z c loses too much in fp64, or that floor cannot be told
-      // from the maximum in fp32 (huge or infinite logits, huge temperatures),
-      // each weight is computed by itself.
-      const float floor = (float)((double)mt - 500.0 / c);
-      const bool plain = fabs((double)mt) * c < 4096.0 && floor < mt && floor > -INFINITY;
-      if (SUM == SUM_F32 && plain) {
-        // z - mt is exact for bf16 logits (2^-24 relative for fp32 ones), the
-        // product with c off by 2^-23 |x| in all, the exponential by 2^-23
-        // relative: a term is exact to (0.7 |x| + 1) 2^-23.  Eight terms are
+      const double mc = (double)mt * c;
+      if (SUM == SUM_F32 && fabs(mc) < 4096.0 && c > 0x1p-100 && c < 0x1p100) {
+        // The exponents z c + shift, shift near -mt c; what is left, 2^-(mt c +
+        // shift), scales the sum.  An exponent x is off by 2^-24 |x| from its
+        // rounding and as much from c's, the exponential by 2^-23 relative: a term
+        // is exact to (0.7 |x| + 1) 2^-23.  -inf and NaN count 0.  Eight terms are
         // added in fp32, then in fp64.
-        const float c32 = (float)c;
+        const float c32 = (float)c, shift = -(float)mc;
 #pragma unroll
         for (int u = 0; u < OCTS; ++u) {
           keep_raw(raw[u]);
@@ -494,24 +494,39 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
           unpack(raw[u], z);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            e[j] = __builtin_amdgcn_exp2f((fmaxf(z[j], floor) - mt) * c32);
+            e[j] = __builtin_amdgcn_exp2f(fmaxf(__builtin_fmaf(z[j], c32, shift), -500.f));
           s += (double)tree_sum8(e);
           __builtin_amdgcn_sched_barrier(0);        // one octet in flight: registers
         }
-      } else if (plain) {
-        const double shift = -(double)mt * c;
+        s *= TwoTo()(-fma((double)mt, (double)c32, (double)shift));
+      } else if (SUM == SUM_F64 && fabs(mc) < 4096.0) {
+        // Here shift is a multiple of 1/64: z c added to `magic` is rounded to
+        // such a multiple as well.  Logits 500 octaves and more below the maximum
+        // (and -inf, NaN) count 2^-500.
+        double opaque = c;                          // its reciprocal is not kept
+        asm volatile("" : "+v"(opaque));
+        const double floor = (double)mt - 500.0 * __builtin_amdgcn_rcp(opaque);
+        const double shift = -rint(mc * kExpTable) / kExpTable;
+        const double magic = kExpRound + shift;
+        const TwoTo two_to;
 #pragma unroll
         for (int u = 0; u < OCTS; ++u) {
           keep_raw(raw[u]);
           float z[8];
           unpack(raw[u], z);
+          const auto add = [&](float z, double& sum) {
+            const double x = fmax((double)z, floor), y = fma(x, c, magic);
+            sum = fma(table_entry(y, table), two_to(fma(x, c, magic - y)), sum);
+          };
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            s += exp2_table<false>(fma((double)fmaxf(z[j], floor), c, shift), table);
-            s1 += exp2_table<false>(fma((double)fmaxf(z[j + 1], floor), c, shift), table);
+            add(z[j], s);
+            add(z[j + 1], s1);
+            if (j == 2) __builtin_amdgcn_sched_barrier(0);   // registers
           }
           __builtin_amdgcn_sched_barrier(0);
         }
+        s = (s + s1) * two_to(-(mc + shift));
       } else if (mt > -INFINITY) {
 #pragma unroll 1
         for (int i = 0; i < OCTS * 8; ++i) {
@@ -519,7 +534,12 @@ __device__ __forceinline__ void stream_tile(const LT* row, int V, int t, double 
           if (e < V) s += weight(clean_logit(logit_at(row, e)), mt, c, table);
         }
       }
-      s = wave_reduce(s + s1, OpAdd());
+      s = wave_reduce(s, OpAdd());
+      if constexpr (OCTS == 8) {                    // the whole tile
+        ref = mt;
+        sum = s;
+        continue;
+      }
       if (mt > ref) {
         sum *= ref > -INFINITY ? weight(ref, mt, c, table) : 0.0;
         ref = mt;
@@ -545,12 +565,14 @@ template <int THREADS>
 __device__ __forceinline__ void load_streamed(const FilterLaunch& A, long r, int groups, int tiles,
                                               bool sum, uint16_t* gm, RowShared<THREADS>& sh,
                                               float& top) {
+  int t0 = threadIdx.x;
+  asm volatile("" : "+v"(t0));                      // its addresses are not kept past this
   // groups is even: a pair of keys at a time
   const uint32_t* g = reinterpret_cast<const uint32_t*>(A.group_key + r * groups);
-  for (int i = threadIdx.x; i < groups / 2; i += THREADS) reinterpret_cast<uint32_t*>(gm)[i] = g[i];
-  for (int t = threadIdx.x; t < tiles; t += THREADS) top = fmaxf(top, A.tile_max[r * tiles + t]);
+  for (int i = t0; i < groups / 2; i += THREADS) reinterpret_cast<uint32_t*>(gm)[i] = g[i];
+  for (int t = t0; t < tiles; t += THREADS) top = fmaxf(top, A.tile_max[r * tiles + t]);
   if (sum)
-    for (int t = threadIdx.x; t < tiles; t += THREADS) {
+    for (int t = t0; t < tiles; t += THREADS) {
       sh.tile_m[t] = A.tile_max[r * tiles + t];
       sh.tile_s[t] = A.tile_sum[r * tiles + t];
     }
@@ -830,7 +852,7 @@ __device__ __forceinline__ int ties_below(double target, double before, double w
 // target may be off; complete: the list holds every kept token.  Also got, the
 // sum of the candidates' weights.
 //
-// Weights are integers in units of 2^-50 here (sums of 2048 of them fit 62
+// Weights are integers in units of 2^-50 here (sums of 4096 of them fit 62
 // bits and are exact whatever their order).
 template <typename LT, int THREADS>
 __device__ __forceinline__ ListCut cut_list(RowShared<THREADS>& sh, int n, const FilterSettings& s,
@@ -951,7 +973,7 @@ __device__ __forceinline__ ListCut cut_list(RowShared<THREADS>& sh, int n, const
   f.n_kept = (int)count;
   if (draw) {
     const uint32_t t = digit_search<THREADS, true>(n, id_bits, id, mass,
-                                                   (double)u * (double)total, sh.bucket, before,
+                                                   (double)uniform(u) * (double)total, sh.bucket, before,
                                                    inside);
     if (threadIdx.x == 0) sh.token = (int)t;
     __syncthreads();
@@ -1013,8 +1035,8 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
         const double run = i ? run1 : run0;
         const bool in = 2 * l + i < nk && w[i] >= s.mp;
         k[i] = in && (s.p >= 1.0 || run < target - slack);
-        keep += k[i];
         most += in && (s.p >= 1.0 || run < target + slack);
+        keep += k[i];
       }
       keep = wave_reduce(keep, OpAdd());
       if (slack > 0.0) {
@@ -1045,7 +1067,7 @@ __device__ __forceinline__ ListCut cut_short_list(RowShared<THREADS>& sh, int n,
 #pragma unroll
           for (int i = 0; i < 2; ++i) x[i] = 2 * l + i < keep ? so.w[2 * l + i] : 0.0;
           const double at = wave_prefix(x[0] + x[1]);
-          const double goal = (double)u * of_lane(at, kWave - 1);
+          const double goal = (double)uniform(u) * of_lane(at, kWave - 1);
           const double before = at - (x[0] + x[1]);
           int first = INT32_MAX, any = -1;
           if (x[0] > 0.0) { any = 2 * l; if (before + x[0] > goal) first = 2 * l; }
@@ -1090,14 +1112,15 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
   const bool nucleus = need_sum && !s.off;
   count = -1;
   if (by_k && !all && s.k > kMaxListK) return false;
-  // The sum of a nucleus row is first taken in fp32 (unless a kernel of its own
-  // took it in fp64), and again in fp64 where its error could move the cut.
+  // The sum of a nucleus row of bf16 is first taken in fp32 (unless a kernel of
+  // its own took it in fp64), and again in fp64 where its error could move the cut.
+  constexpr bool TWICE = !PRE && sizeof(LT) == 2;
 #pragma unroll 1
-  for (bool exact = PRE || !nucleus;; exact = true) {
+  for (bool exact = !TWICE || !nucleus;; exact = true) {
     float top = -INFINITY;
     if constexpr (PRE) load_streamed<THREADS>(A, r, groups, tiles, need_sum, gm, sh, top);
     else if (!need_sum) stream_row<LT, THREADS, NO_SUM>(row, V, s.c, G, gm, sh, top);
-    else if (exact) stream_row<LT, THREADS, SUM_F64>(row, V, s.c, G, gm, sh, top);
+    else if (!TWICE || exact) stream_row<LT, THREADS, SUM_F64>(row, V, s.c, G, gm, sh, top);
     else stream_row<LT, THREADS, SUM_F32>(row, V, s.c, G, gm, sh, top);
     const float m = block_reduce<THREADS>(top, reinterpret_cast<float*>(sh.redi), OpMax());
     f = sv_filter_row{s.c, 0.0, m, INFINITY, -1, 0};
@@ -1123,14 +1146,14 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
     }
     // The fp32 sum's error: 2^-19 covers terms of |x| < 20; those below weigh
     // under 2^-20.
-    const double slack = exact ? 0.0 : s.p * S * 0x1p-19;
+    const double slack = !TWICE || exact ? 0.0 : s.p * S * 0x1p-19;
     // the lowest key a kept token can have
     const uint32_t kmax = logit_key(m);
     uint32_t mp_key = kKeyNegInf + 1;
     if (s.mp > 0.0 && s.c > 0.0) {
       // z >= m + log2(min_p) / c, a little lower: the exact test follows
       const float z =
-          (float)((double)m + ((double)__builtin_amdgcn_logf((float)s.mp) - 1e-4) / s.c);
+          (float)((double)m + ((double)__builtin_amdgcn_logf(uniform(s.mp)) - 1e-4) / s.c);
       mp_key = max(mp_key, min(kmax, logit_key(clean_logit(z)) - 2));
     }
     bool complete = true;                           // the list holds every kept token
@@ -1203,7 +1226,7 @@ __device__ __forceinline__ int find_tile(const double* mass, int tiles, float u,
     mine += x[i];
   }
   const double incl = wave_prefix(mine);
-  target = (double)u * of_lane(incl, kWave - 1);
+  target = (double)uniform(u) * of_lane(incl, kWave - 1);
   double run = incl - mine, at = 0.0;
   int hit = -1, any = -1;
 #pragma unroll
@@ -1266,7 +1289,7 @@ __device__ __forceinline__ int draw_tiles(const LT* row, int V, RowShared<THREAD
 constexpr int kStreamThreads = 256;
 template <typename LT>
 __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLaunch A) {
-  __shared__ double table[kExpTable];
+  __shared__ ExpEntry table[kExpTable];
   const long r = blockIdx.x;
   const int V = A.V, G = A.group_octets;
   const int tiles = (V + kRowTile - 1) / kRowTile;
@@ -1278,7 +1301,7 @@ __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLau
   const LT* row = static_cast<const LT*>(A.logits) + ri * A.row_stride;
   const bool sum = row_needs_sum(s, V);
   if (sum) {                                        // uniform
-    fill_exp_table(table, threadIdx.x, kStreamThreads);
+    fill_exp_table(table);
     __syncthreads();
   }
   const int t = blockIdx.y * (kStreamThreads / kWave) + threadIdx.x / kWave;
@@ -1298,7 +1321,7 @@ __global__ __launch_bounds__(kStreamThreads) void filter_stream_kernel(FilterLau
 template <int THREADS>
 __device__ __forceinline__ uint16_t* row_shared(unsigned char* lds, int cap, RowShared<THREADS>& sh) {
   unsigned long long* list = reinterpret_cast<unsigned long long*>(lds + sizeof(RowShared<THREADS>));
-  fill_exp_table(sh.table, threadIdx.x, THREADS);
+  fill_exp_table(sh.table);
   if (threadIdx.x == 0) {
     sh.list = list;
     sh.cap = cap;
@@ -1343,8 +1366,12 @@ filter_rows_kernel(FilterLaunch A) {
   const int b = (int)(r / A.per_seq);
   const int V = A.V;
   int errors = 0;
-  const FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps,
+  FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps,
                                            A.min_ps, b, V, errors);
+  s.c = uniform(s.c);
+  s.p = uniform(s.p);
+  s.mp = uniform(s.mp);
+  s.k = uniform(s.k);
   const long ri = A.row_index ? (long)A.row_index[r] : r;
   const bool there = ri >= 0 && ri < A.n_rows;
   sv_filter_row f{0.0, 0.0, -INFINITY, INFINITY, -1, 0};
@@ -1572,7 +1599,7 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
 template <typename LT, bool QL>
 __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerifyLaunch A) {
   constexpr int WAVES = kVerifyThreads / kWave;
-  __shared__ double table[kExpTable];
+  __shared__ ExpEntry table[kExpTable];
   __shared__ double red[WAVES];
   __shared__ int redi[WAVES];
   __shared__ double mass[kRowTiles];
@@ -1581,7 +1608,7 @@ __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerify
   const int K = A.K, V = A.V;
   const int tiles = (V + kRowTile - 1) / kRowTile, parts = (tiles + WAVES - 1) / WAVES;
   if ((long)blockIdx.x >= (long)pending * parts) return;
-  fill_exp_table(table, threadIdx.x, kVerifyThreads);
+  fill_exp_table(table);
   __syncthreads();
   const int w = threadIdx.x / kWave, l = lane_id();
   for (long item = blockIdx.x; item < (long)pending * parts; item += gridDim.x) {

@@ -4,9 +4,10 @@ oracle.
 Kept sets (the filter rows' integers and logits) and tokens must be equal to
 the oracle's: both sides evaluate every cut and draw in fp64, so only a
 decision within NEAR of its threshold may differ, and none of the seeded
-decisions lies that close unless a check says so.  NEAR: at most 2^19 weights of
-relative error 2^-45 (the coarsest rounding anywhere) stay below 2^-26 of a sum
-in the worst case, and around 2^-35 when the roundings are independent.
+decisions lies that close unless a check says so.  NEAR: the weights of the long
+sums are exact to 5e-12 (2^-37), all others to 1e-14, and so are a sum and a
+share of it; the units of integer masses are 2^-50 of the largest, for 2^12 of
+them 2^-38 at most.
 Probabilities are fp64 rounded once to fp32: half a step, 2^-24 relative, plus
 fp64 noise far below it.
 """
@@ -454,3 +455,98 @@ def test_refusals(gpu):
                                     torch.zeros((2, 1, 8), dtype=torch.int32, device=DEV),
                                     torch.zeros((2, 1), dtype=torch.int32, device=DEV),
                                     torch.zeros((2, 2), device=DEV), T)
+
+
+# ---------------------------------------------------------------- many rows
+# More rows than compute units: one kernel streams and cuts each row, rows
+# without a candidate list follow in a second.
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("V", [777, 5003, 20011])
+def test_sampler_many_rows(gpu, V, bf16):
+    rng = np.random.default_rng(V + 1)
+    n = 3 * len(KINDS) * len(SETTINGS)
+    z = make_rows(rng, n, V, bf16, KINDS)
+    check_sample(gpu, z, bf16, [i // len(KINDS) for i in range(n)],
+                 rng.random((n, 1), dtype=np.float32))
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_sampler_many_large_rows(gpu, bf16):
+    rng = np.random.default_rng(77)
+    n, V = 528, 70001
+    z = make_rows(rng, n, V, bf16, ("normal", "flat", "ties", "masked", "none", "inf", "lowest"))
+    check_sample(gpu, z, bf16, [i // 7 for i in range(n)], rng.random((n, 1), dtype=np.float32),
+                 probs=False)
+
+
+@pytest.mark.parametrize("kind", ["none", "inf", "lowest", "equal", "one", "nan", "zeros"])
+def test_sampler_few_large_rows_of_extremes(gpu, kind):
+    """Rows that a kernel of their own streams (few, longer than 65536)."""
+    rng = np.random.default_rng(78)
+    n, V = len(SETTINGS), 66001
+    for bf16 in (True, False):
+        z = make_rows(rng, n, V, bf16, (kind,))
+        check_sample(gpu, z, bf16, range(n), rng.random((n, 1), dtype=np.float32), probs=False)
+
+
+@pytest.mark.parametrize("dense", [True, False])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_verify_many_rows(gpu, bf16, dense):
+    rng = np.random.default_rng(79)
+    B, K, V = 130, 4, 4099
+    zt, zd = verify_case(rng, B, K, V, bf16, kinds=("normal", "flat", "ties", "masked", "lowest"))
+    check_verify(gpu, zt, zd, B, K, V, bf16, range(B), rng, dense, stride=V + 1)
+
+
+def test_verify_many_large_rows(gpu):
+    rng = np.random.default_rng(80)
+    B, K, V = 176, 2, 33333
+    zt, zd = verify_case(rng, B, K, V, True, noise=0.1, kinds=("normal", "flat"))
+    check_verify(gpu, zt, zd, B, K, V, True, range(B), rng, False)
+
+
+def test_verify_graph_and_streams(gpu):
+    """A captured draft and verify replayed on new inputs, and on two streams at once."""
+    rng = np.random.default_rng(81)
+    B, K, V = 24, 3, 20000
+    _, kw = settings_of(range(B))
+
+    def step(i):
+        tok, q, rows = gpu.spec_draft_sample_filtered(i[1], K, uniforms=i[3], want_filter_rows=True,
+                                                      **kw)
+        out, acc, _ = gpu.spec_verify_filtered_lq(i[0].view(B, K + 1, V), i[1], rows, tok, i[2],
+                                                  **kw)
+        return tok, rows, out, acc
+
+    sets = []
+    for _ in range(3):
+        zt, zd = verify_case(rng, B, K, V, True)
+        sets.append([dev(zt), dev(zd), dev(rng.random((B, K + 1), dtype=np.float32)),
+                     dev(rng.random((B, K), dtype=np.float32))])
+    eager = [step(i) for i in sets]
+    static = [t.clone() for t in sets[0]]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(static)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        res = step(static)
+    for i in (1, 2, 0, 2):
+        for a, b in zip(static, sets[i]):
+            a.copy_(b)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(res, eager[i]))
+        step(sets[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    torch.cuda.synchronize()
+    for rep in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append((i, step(sets[i])))
+    torch.cuda.synchronize()
+    for i, r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, eager[i]))
