@@ -363,7 +363,7 @@ constexpr int kGroupsFew = 10240;      // ... elsewhere
 template <int THREADS>
 struct RowShared {
   union {
-    struct { uint32_t cnt[kTopBins], mass[kTopBins]; } top;
+    unsigned long long top[kTopBins];  // groups << 32 | their weights in 2^-18
     uint16_t queue[kQueue];
     unsigned long long bucket[kBuckets];
     struct { unsigned long long entry[kWaveList]; double w[kWaveList]; int id[kWaveList]; } sorted;
@@ -601,21 +601,29 @@ __device__ __forceinline__ uint32_t threshold_key(const uint16_t* gm, int groups
   for (int level = 0; level < 3; ++level) {
     const int shift = hi - lo < kTopBins ? 0 : 8;
     __syncthreads();
-    for (int i = threadIdx.x; i < kTopBins; i += THREADS) sh.top.cnt[i] = sh.top.mass[i] = 0;
+    for (int i = threadIdx.x; i < kTopBins; i += THREADS) sh.top[i] = 0;
     if (threadIdx.x == 0) sh.bin = -1;
     __syncthreads();
+    // four keys at a time (groups are whole tiles'); by mass, one LDS addition
+    // counts a group and its weight, and weights under 2^-18 are left out
+    const uint32_t least =
+        by_mass ? max(lo, logit_key(clean_logit(z0 - 18.f / uniform(c))) >> 16) : lo;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < groups; i += THREADS) {
-      const uint32_t key = gm[i];
-      if (key <= hi && key >= lo) {
-        const uint32_t b = (hi - key) >> shift;
-        atomicAdd(&sh.top.cnt[b], 1u);
-        if (by_mass) {
-          // the logit: exactly (bf16), or the middle of those with this half of a key
-          const float g = key_logit(key << 16 | (sizeof(LT) == 4 ? 0x8000u
-                                                 : key & 0x8000u ? 0u : 0xffffu));
-          atomicAdd(&sh.top.mass[b],
-                    g >= z0 ? 262144u : (uint32_t)(__builtin_amdgcn_exp2f((g - z0) * c) * 262144.f));
+    for (int i = threadIdx.x; i < groups / 4; i += THREADS) {
+      const uint2 keys = reinterpret_cast<const uint2*>(gm)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t two = j < 2 ? keys.x : keys.y, key = j % 2 ? two >> 16 : two & 0xffffu;
+        if (key <= hi && key >= least) {
+          uint32_t w = 0;
+          if (by_mass) {
+            // the logit: exactly (bf16), or the middle of those with this half of a key
+            const float g = key_logit(key << 16 | (sizeof(LT) == 4 ? 0x8000u
+                                                   : key & 0x8000u ? 0u : 0xffffu));
+            w = g >= z0 ? 262144u
+                        : (uint32_t)(__builtin_amdgcn_exp2f((g - z0) * c) * 262144.f);
+          }
+          atomicAdd(&sh.top[(hi - key) >> shift], 1ull << 32 | w);
         }
       }
     }
@@ -625,7 +633,7 @@ __device__ __forceinline__ uint32_t threshold_key(const uint16_t* gm, int groups
       const int l = lane_id();
       int n[PER], mine = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) { n[i] = sh.top.cnt[l * PER + i]; mine += n[i]; }
+      for (int i = 0; i < PER; ++i) { n[i] = (int)(sh.top[l * PER + i] >> 32); mine += n[i]; }
       int run = wave_prefix(mine) + above - mine;
       int hit = -1, before = 0;
       float fbefore = 0.f;
@@ -642,7 +650,7 @@ __device__ __forceinline__ uint32_t threshold_key(const uint16_t* gm, int groups
         int r = run;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const float x = (float)sh.top.mass[l * PER + i] * (1.f / 262144.f) * (float)groups;
+          const float x = (float)(uint32_t)sh.top[l * PER + i] * (1.f / 262144.f) * (float)groups;
           const float left = (float)max(1, groups - r), after = (float)max(1, groups - r - n[i]);
           most[i] = x * __builtin_amdgcn_rcpf(after);
           f[i] = n[i] ? x * 0.69314718f *
@@ -683,7 +691,7 @@ __device__ __forceinline__ uint32_t threshold_key(const uint16_t* gm, int groups
     near = false;
     above = uniform(sh.above);
     mass = uniform(sh.frac);
-    const int in = (int)uniform(sh.top.cnt[b]);
+    const int in = (int)(uniform(sh.top[b]) >> 32);
     const uint32_t top = hi - ((uint32_t)b << shift);
     const uint32_t bottom = top - lo > 255 ? top - 255 : lo;
     if (in <= above / 4 + 32) return bottom;
@@ -1165,15 +1173,16 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
     for (int attempt = 0; attempt < 8; ++attempt) {
       if (!all) {
         if (by_k || nucleus) {
-          // A nucleus row's share p of the sum is estimated from the group
-          // maxima; what the tokens found lack of it, and a tenth more, from
-          // those below.  Heavy tokens behind heavier ones of their group are
+          // A nucleus row's share p of the sum, and a tenth of the rest, is
+          // estimated from the group maxima (without that tenth half of the rows
+          // need a second turn: 60 against 50 us for 64 rows); what the tokens
+          // found lack of it, and a tenth more, from those below.  Heavy tokens behind heavier ones of their group are
           // missing from the first estimate: where it gave too many tokens,
           // those of the kFirst largest groups come first.
           const bool est = nucleus && !first, more = est && got > 0.0;
           const int k = nucleus ? (est ? 0 : min(kFirst, groups)) : s.k;
           const float z0 = more ? key_logit(kt) : m;
-          const double lack = more ? 1.1 * (s.p * S - got) : s.p * S;
+          const double lack = more ? 1.1 * (s.p * S - got) : (0.9f * uniform(s.p) + 0.1f) * S;
           const float aim = est ? (float)(lack / weight(z0, m, s.c, sh.table)) : 0.f;
           kt = (s.k == 1 ? kmax >> 16
                          : threshold_key<LT, THREADS>(
@@ -1594,25 +1603,25 @@ __global__ __launch_bounds__(kVerifyThreads) void filtered_verify_kernel(Filtere
 
 // The new tokens of the sequences whose row a has no list (no filter, or a
 // nucleus of thousands): the residual's and p's mass of every tile of the row,
-// one wave per tile over all CUs; the workgroup that finishes a sequence's last
-// tiles finds the token.
+// one workgroup per tile over all CUs; the one that finishes a sequence's last
+// tile finds the token.
 template <typename LT, bool QL>
 __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerifyLaunch A) {
-  constexpr int WAVES = kVerifyThreads / kWave;
+  constexpr int WAVES = kVerifyThreads / kWave, OCTS = kRowTile / kTile / WAVES;
   __shared__ ExpEntry table[kExpTable];
-  __shared__ double red[WAVES];
+  __shared__ double red[WAVES], red2[WAVES];
   __shared__ int redi[WAVES];
   __shared__ double mass[kRowTiles];
   __shared__ int sh_last;
   const int pending = A.pending[0];
   const int K = A.K, V = A.V;
-  const int tiles = (V + kRowTile - 1) / kRowTile, parts = (tiles + WAVES - 1) / WAVES;
-  if ((long)blockIdx.x >= (long)pending * parts) return;
+  const int tiles = (V + kRowTile - 1) / kRowTile;
+  if ((long)blockIdx.x >= (long)pending * tiles) return;
   fill_exp_table(table);
   __syncthreads();
   const int w = threadIdx.x / kWave, l = lane_id();
-  for (long item = blockIdx.x; item < (long)pending * parts; item += gridDim.x) {
-    const int b = A.pending[1 + item / parts];
+  for (long item = blockIdx.x; item < (long)pending * tiles; item += gridDim.x) {
+    const int b = A.pending[1 + item / tiles];
     const long row0 = (long)b * (K + 1);
     const int a = A.out_num_accepted[b];
     const sv_filter_row f = A.rows[row0 + a];
@@ -1641,63 +1650,61 @@ __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerify
       const double p = p_at(logit_at(za, x), x);
       return p > 0.0 ? fmax(0.0, p - q_at(x)) : 0.0;
     };
-    const int t = (int)(item % parts) * WAVES + w;
-    if (t < tiles) {
-      double rs = 0.0, ps = 0.0;
-      // two octets of the row and of q at a time
-#pragma unroll 1
-      for (int u = 0; u < 8; u += 2) {
-        Raw<LT> rz[2], rq[2];
-        float qf[2][8];
-        const int e0 = t * kRowTile + u * kTile + 8 * l;
+    const int t = (int)(item % tiles);
+    double rs = 0.0, ps = 0.0;
+    // a lane's octets of the tile and of q together
+    Raw<LT> rz[OCTS], rq[OCTS];
+    float qf[OCTS][8];
+    const int e0 = t * kRowTile + w * OCTS * kTile + 8 * l;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int e = e0 + i * kTile;
-          if (e + 8 <= V) raw8(za + e, rz[i]);
-          else raw8_end(za, e, V, rz[i]);
-          if (residual) {
-            if constexpr (QL) {
-              if (q.logits) {
-                if (e + 8 <= V) raw8(q.logits + e, rq[i]);
-                else raw8_end(q.logits, e, V, rq[i]);
-              }
-            } else if (e + 8 <= V) {
-              load8(q.probs + e, qf[i]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) qf[i][j] = e + j < V ? q.probs[e + j] : 0.f;
-            }
+    for (int i = 0; i < OCTS; ++i) {
+      const int e = e0 + i * kTile;
+      if (e + 8 <= V) raw8(za + e, rz[i]);
+      else raw8_end(za, e, V, rz[i]);
+      if (residual) {
+        if constexpr (QL) {
+          if (q.logits) {
+            if (e + 8 <= V) raw8(q.logits + e, rq[i]);
+            else raw8_end(q.logits, e, V, rq[i]);
           }
-        }
+        } else if (e + 8 <= V) {
+          load8(q.probs + e, qf[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int e = e0 + i * kTile;
-          float z[8], zq[8];
-          unpack(rz[i], z);
-          if constexpr (QL) unpack(rq[i], zq);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const double p = e + j < V ? p_at(z[j], e + j) : 0.0;
-            ps += p;
-            if (residual && p > 0.0) {
-              double x;
-              if constexpr (QL) x = q.logits ? q_of(zq[j], e + j) : 0.0;
-              else x = (double)qf[i][j];
-              rs += fmax(0.0, p - x);
-            }
-          }
+          for (int j = 0; j < 8; ++j) qf[i][j] = e + j < V ? q.probs[e + j] : 0.f;
         }
       }
-      rs = wave_reduce(rs, OpAdd());
-      ps = wave_reduce(ps, OpAdd());
-      if (l == 0) {
-        st_coherent(rmass + t, rs);
-        st_coherent(pmass + t, ps);
-      }
-      wait_stores_performed();
     }
+#pragma unroll
+    for (int i = 0; i < OCTS; ++i) {
+      const int e = e0 + i * kTile;
+      float z[8], zq[8];
+      unpack(rz[i], z);
+      if constexpr (QL) unpack(rq[i], zq);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double p = e + j < V ? p_at(z[j], e + j) : 0.0;
+        ps += p;
+        if (residual && p > 0.0) {
+          double x;
+          if constexpr (QL) x = q.logits ? q_of(zq[j], e + j) : 0.0;
+          else x = (double)qf[i][j];
+          rs += fmax(0.0, p - x);
+        }
+      }
+    }
+    rs = wave_reduce(rs, OpAdd());
+    ps = wave_reduce(ps, OpAdd());
+    if (l == 0) { red[w] = rs; red2[w] = ps; }
     __syncthreads();
-    if (threadIdx.x == 0) sh_last = atomicAdd(&A.done[b], 1) == parts - 1;
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int i = 1; i < WAVES; ++i) { rs += red[i]; ps += red2[i]; }
+      st_coherent(rmass + t, rs);
+      st_coherent(pmass + t, ps);
+      wait_stores_performed();
+      sh_last = atomicAdd(&A.done[b], 1) == tiles - 1;
+    }
     __syncthreads();
     if (sh_last) {                                   // uniform
       const float u = A.uniforms[row0 + K];
@@ -1815,10 +1822,9 @@ hipError_t launch_verify_tail(const FilteredVerifyLaunch& L, hipStream_t stream)
   trace_after(stream, SV_KERNEL_FILTERED_VERIFY);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && L.V > kCand) {              // a shorter row always has a list
-    const int waves = kVerifyThreads / kWave;
-    const long parts = ((L.V + kRowTile - 1) / kRowTile + waves - 1) / waves;
+    const long tiles = (L.V + kRowTile - 1) / kRowTile;
     trace_before(stream, SV_KERNEL_FILTERED_VERIFY);
-    residual_kernel<LT, QL><<<dim3((unsigned)std::min(L.B * parts, 2048L)), kVerifyThreads, 0,
+    residual_kernel<LT, QL><<<dim3((unsigned)std::min(L.B * tiles, 2048L)), kVerifyThreads, 0,
                               stream>>>(L);
     trace_after(stream, SV_KERNEL_FILTERED_VERIFY);
     e = hipGetLastError();
