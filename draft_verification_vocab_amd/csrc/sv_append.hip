@@ -23,7 +23,9 @@ namespace sv {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendLds = 4096;      // (cos, sin) pairs per workgroup
+// (cos, sin) pairs per workgroup: 16 KB, so that eight workgroups fit a CU (with
+// 32 KB five do: 66 against 56 us for 1024 drafts of 7 rows into e4m3)
+constexpr int kAppendLds = 2048;
 constexpr int kAppendRows = 16;       // most rows of a workgroup
 
 // n / d for n * d < 2^32 with magic = ceil(2^32 / d).
