@@ -3,12 +3,29 @@
 // sampler) or used as the target of rejection sampling (the verify).  The
 // definitions are in sv_filter.h and include/spec_verify.h.
 //
-//   filter_rows_kernel   one workgroup per row: the row's kept set as a
-//                        filter row (its last token, maximum and 1 / sum), and
-//                        for the sampler the drawn token and the dense q;
-//   filtered_verify_kernel  one workgroup per sequence: the accept scan from
-//                        the filter rows, then the residual draw on the row
-//                        of the first rejection.
+//   filter_rows_kernel     one workgroup per row: the row's kept set as a filter
+//                          row (its last token, maximum and 1 / sum), and for
+//                          the sampler the drawn token and the dense q;
+//   filter_stream_kernel   before it where rows are few and long: the pass over
+//                          the logits by all CUs;
+//   filter_general_kernel  after it where rows are many: those whose kept set
+//                          does not fit the candidate list;
+//   filtered_verify_kernel one workgroup per sequence: the accept scan from the
+//                          filter rows, then the residual draw on the list of
+//                          the row of the first rejection;
+//   residual_kernel        that draw where the row has no list, over all CUs.
+//
+// The cuts are exact without a sort: a threshold from the groups' maxima picks
+// some hundred candidates, their weights become integers, and the cut and the
+// draw are found digit by digit in sums that do not depend on their order.
+// What bounds it (MI355X, vocabulary 151936 in bf16):
+//   many rows   HBM, then the exponentials: 7168 rows (2.18 GB) take 395-455 us
+//               under top-k, min-p or greedy settings (4.8 to 5.5 TB/s), 690-780
+//               under top-p alone (fp32 sums), 860-900 without a filter (fp64
+//               sums, whose multiplications take two turns each); mixed 540-580;
+//   few rows    the chain of steps of one workgroup: streaming or loading the
+//               groups 4 us, threshold 2-5, candidates 3-6, cut and draw 3-9;
+//               one row 15 us in all, 256 rows 74 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -411,9 +428,10 @@ __device__ __forceinline__ bool row_needs_sum(const FilterSettings& s, int V) {
   return V > kCand && s.k >= V && (s.p < 1.0 || s.off);
 }
 
-// How the stream takes it.  By workgroups of rows SUM_F32 takes 0.6 of SUM_F64's
-// time for a nucleus row (650 against 1000 us for 7168 rows of 151936), and one row
-// in a hundred has to be streamed again for its cut.
+// How the stream takes it.  For 7168 nucleus rows of 151936 in bf16 SUM_F32 takes
+// 690-780 us against 990-1050 of SUM_F64, though about one row in a hundred has to
+// be streamed again for its cut.  For few rows that one row costs all (79 against
+// 59 us for 64); rows of fp32 wait for memory twice as long and keep SUM_F64.
 enum RowSum { NO_SUM, SUM_F32, SUM_F64 };
 
 // The maximum over N = 2, 4 or 8 adjacent lanes (from the maximum over N / 2,
