@@ -767,6 +767,10 @@ SV_API sv_status peagle_append_kv(
       value_stride < (int64_t)kv_heads * head_dim || block_stride < 0 || slot_stride < 0 ||
       head_stride < 0)
     return SV_ERR_SHAPE;
+  // heads of different slots or blocks that share memory
+  if ((kv_heads > 1 && head_stride < head_dim) || (block_size > 1 && slot_stride < head_dim) ||
+      (num_blocks > 1 && block_stride < head_dim))
+    return SV_ERR_SHAPE;
   if (q_heads > 0 && (query_stride < (int64_t)q_heads * head_dim ||
                       out_query_stride < (int64_t)q_heads * head_dim))
     return SV_ERR_SHAPE;

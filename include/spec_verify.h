@@ -631,7 +631,8 @@ typedef struct sv_filter_row {
 
 /* Bytes of device workspace a filtered call needs for n_rows logit rows (B*K
  * rows of the sampler, B*(K+1) of the verify).  Its contents do not matter and
- * are not kept between calls.  Returns 0 for invalid sizes. */
+ * are not kept between calls, so it must not be one of those that the calls
+ * above want zero-filled.  Returns 0 for invalid sizes. */
 SV_API size_t spec_filter_workspace_bytes(int64_t n_rows, int V);
 
 /*
@@ -735,6 +736,8 @@ SV_API sv_status spec_verify_filtered_lq(
  *                    + s * slot_stride + h * head_stride + d, so that caches
  *                    with the heads outside the slots and halves of one
  *                    key-and-value buffer are addressed in place.
+ *                    Strides of dimensions longer than 1 are at least
+ *                    head_dim; entries must not overlap.
  *   cache_dtype      dtype, or SV_E4M3: round(x / scale[h]) limited to +-448
  *                    (NaN stays NaN).
  *   k_scales, v_scales  optional [kv_heads] fp32 (NULL: 1), SV_E4M3 only.

@@ -109,3 +109,14 @@ def test_append_checks(lib):
                 dict(oq=FAKE + 1), dict(cd=3, ksc=FAKE + 1), dict(cd=3, vsc=FAKE + 2),
                 dict(err=FAKE + 2)):
         assert append(lib, **bad) == EALIGN, bad
+
+
+def test_append_refuses_caches_that_overlap_themselves(lib):
+    """Strides below head_dim where the dimension is longer than 1; any stride where it is not."""
+    base = dict(R=0)
+    assert append(lib, **base) == OK
+    for st in ((2048, 128, 63), (2048, 63, 64), (63, 128, 64), (0, 128, 64), (2048, 0, 64)):
+        assert append(lib, st=st, **base) == ESHAPE, st
+    assert append(lib, Hkv=1, st=(2048, 128, 0), **base) == OK
+    assert append(lib, nb=1, st=(0, 128, 64), **base) == OK
+    assert append(lib, bs=1, st=(2048, 0, 64), **base) == OK

@@ -302,3 +302,12 @@ def test_decode_round(gpu):
     full_v[slots[ok]] = x[:, Hkv:][ok]
     assert np.array_equal(f64(vc).reshape(full_v.shape), full_v)
     assert np.allclose(f64(kc).reshape(full_k.shape), full_k, rtol=2.0 ** -8 * 1.001, atol=1e-5)
+
+
+def test_refuses_an_expanded_cache(gpu):
+    k = torch.zeros((4, 2, 64), device=DEV).bfloat16()
+    pos = torch.arange(4, device=DEV)
+    one = torch.zeros((1, 16, 2, 64), device=DEV).bfloat16()
+    with pytest.raises(gpu.SpecVerifyError):
+        gpu.peagle_append_kv(k, k, pos, pos, one.expand(3, 16, 2, 64), one.expand(3, 16, 2, 64))
+    assert not one.any()

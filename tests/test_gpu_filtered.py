@@ -550,3 +550,28 @@ def test_verify_graph_and_streams(gpu):
     torch.cuda.synchronize()
     for i, r in got:
         assert all(torch.equal(a, b) for a, b in zip(r, eager[i]))
+
+
+@pytest.mark.parametrize("n,V", [(16, 5003), (16, 66001), (528, 5003)])
+@pytest.mark.parametrize("kind", ["far", "steep", "gentle"])
+def test_sampler_far_and_steep_logits(gpu, n, V, kind):
+    """Logits far from 0 and temperatures at which an exponent's parts leave the
+    range of the fast sums; each weight is then computed by itself."""
+    rng = np.random.default_rng(90)
+    z = (3 * rng.standard_normal((n, V))).astype(np.float32)
+    z += {"far": np.float32(9000.0), "steep": np.float32(-2.0), "gentle": np.float32(1e-3)}[kind]
+    T = {"far": 1.0, "steep": 1e-4, "gentle": 1e6}[kind]
+    u = rng.random((n, 1), dtype=np.float32)
+    p = rng.choice(np.array([1.0, 0.9, 0.5], np.float32), n)
+    for bf16 in (False, True):
+        zz = f32_to_bf16_bits(z) if bf16 else z
+        tok, _, rows = gpu.spec_draft_sample_filtered(
+            dev(zz), 1, uniforms=dev(u), temperatures=dev(np.full(n, T, np.float32)),
+            top_ps=dev(p), want_filter_rows=True)
+        got = {k: v.reshape(-1) for k, v in unpack(rows).items()}
+        tok = tok.cpu().numpy().reshape(-1)
+        for i in range(0, n, max(1, n // 64)):
+            want = F.filter_row(wide(zz[i:i + 1], bf16)[0], float(np.float32(T)), 0, float(p[i]))
+            check_row(got, i, want)
+            t, near = F.draw(want.probs, float(u[i, 0]))
+            assert int(tok[i]) == t or near < NEAR, (i, int(tok[i]), t, near)
