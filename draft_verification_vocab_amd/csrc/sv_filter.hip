@@ -430,8 +430,8 @@ __device__ __forceinline__ bool row_needs_sum(const FilterSettings& s, int V) {
 
 // How the stream takes it.  For 7168 nucleus rows of 151936 in bf16 SUM_F32 takes
 // 690-780 us against 990-1050 of SUM_F64, though about one row in a hundred has to
-// be streamed again for its cut.  For few rows that one row costs all (79 against
-// 59 us for 64); rows of fp32 wait for memory twice as long and keep SUM_F64.
+// be streamed again for its cut; 3584 in fp32 take 464-543 against 619-653 us.  For
+// few rows that one row costs all (79 against 59 us for 64).
 enum RowSum { NO_SUM, SUM_F32, SUM_F64 };
 
 // The maximum over N = 2, 4 or 8 adjacent lanes (from the maximum over N / 2,
@@ -1138,9 +1138,9 @@ __device__ __forceinline__ bool filter_row_list(const FilterLaunch& A, long r, c
   const bool nucleus = need_sum && !s.off;
   count = -1;
   if (by_k && !all && s.k > kMaxListK) return false;
-  // The sum of a nucleus row of bf16 is first taken in fp32 (unless a kernel of
-  // its own took it in fp64), and again in fp64 where its error could move the cut.
-  constexpr bool TWICE = !PRE && sizeof(LT) == 2;
+  // The sum of a nucleus row is first taken in fp32 (unless a kernel of its own
+  // took it in fp64), and again in fp64 where its error could move the cut.
+  constexpr bool TWICE = !PRE;
 #pragma unroll 1
   for (bool exact = !TWICE || !nucleus;; exact = true) {
     float top = -INFINITY;
