@@ -8,8 +8,8 @@
 //                          the sampler the drawn token and the dense q;
 //   filter_stream_kernel   before it where rows are few and long: the pass over
 //                          the logits by all CUs;
-//   filter_general_kernel  after it where rows are many: those whose kept set
-//                          does not fit the candidate list;
+//   filter_left_kernel     after it where rows are many: those whose kept set
+//                          does not fit its candidate list;
 //   filtered_verify_kernel one workgroup per sequence: the accept scan from the
 //                          filter rows, then the residual draw on the list of
 //                          the row of the first rejection;
@@ -1381,20 +1381,17 @@ __device__ __forceinline__ void write_probs(const LT* row, int V, const sv_filte
     __builtin_nontemporal_store((float)row_prob(f, logit_at(row, e), e), q + e);
 }
 
-// One workgroup per row.  PRE: the row was streamed by filter_stream_kernel.
-// GENERAL: rows for the general path are done here, which costs registers and
-// spares a launch; otherwise they are left to filter_general_kernel.
+// Row r by one workgroup.  PRE: the row was streamed by filter_stream_kernel.
+// GENERAL: rows that do not fit the list are done here as well; otherwise they are
+// left to filter_left_kernel.
 template <typename LT, int THREADS, bool PRE, bool GENERAL>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4))) void
-filter_rows_kernel(FilterLaunch A) {
-  extern __shared__ __align__(16) unsigned char lds[];
+__device__ __forceinline__ void filter_one_row(const FilterLaunch& A, long r, unsigned char* lds) {
   RowShared<THREADS>& sh = *reinterpret_cast<RowShared<THREADS>*>(lds);
-  const long r = blockIdx.x;
   const int b = (int)(r / A.per_seq);
   const int V = A.V;
   int errors = 0;
-  FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps,
-                                           A.min_ps, b, V, errors);
+  FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps, A.min_ps,
+                                     b, V, errors);
   s.c = uniform(s.c);
   s.p = uniform(s.p);
   s.mp = uniform(s.mp);
@@ -1457,38 +1454,39 @@ filter_rows_kernel(FilterLaunch A) {
   }
 }
 
-// The rows that filter_rows_kernel left (their counts say so), one workgroup
-// per row in turn.
-constexpr int kGeneralThreads = 1024;
+template <typename LT, int THREADS, bool PRE, bool GENERAL>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4))) void
+filter_rows_kernel(FilterLaunch A) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  filter_one_row<LT, THREADS, PRE, GENERAL>(A, blockIdx.x, lds);
+}
+
+// The rows that filter_rows_kernel left (their counts say so) with a longer list
+// and, where that does not do, by the general path: each workgroup looks at the
+// counts of rows a grid apart, all at once, and takes those left in turn.
+constexpr int kLeftThreads = 512;
 template <typename LT>
-__global__ __launch_bounds__(kGeneralThreads) void filter_general_kernel(FilterLaunch A) {
-  constexpr int THREADS = kGeneralThreads;
-  __shared__ __align__(16) unsigned char
-      lds[sizeof(FilterShared<THREADS>) > sizeof(DrawShared) ? sizeof(FilterShared<THREADS>)
-                                                             : sizeof(DrawShared)];
-  const int V = A.V;
-  const long rows = (long)A.B * A.per_seq;
-  for (long r = blockIdx.x; r < rows; r += gridDim.x) {
-    if (A.list_counts[r] != kGeneralRow) continue;
-    int errors = 0;
-    const FilterSettings s = filter_settings(A.temperatures, A.temperature, A.top_ks, A.top_ps,
-                                             A.min_ps, (int)(r / A.per_seq), V, errors);
-    const LT* row = static_cast<const LT*>(A.logits) +
-                    (A.row_index ? (long)A.row_index[r] : r) * A.row_stride;
-    const bool sampled = A.out_tokens && s.c != 0.0;
-    // a barrier before anything is written: every thread has read the count
-    int token;
-    const sv_filter_row f = general_row<LT, THREADS>(
-        row, V, s, sampled, sampled ? A.uniforms[r] : 0.f, lds, token);
-    if (f.n_kept == 0) errors |= SV_DEVERR_EMPTY_ROW;
-    else if (s.c == 0.0) token = f.last;
-    if (threadIdx.x == 0) {
-      if (errors) flag_error(A.device_error, errors);
-      if (A.out_rows) A.out_rows[r] = f;
-      if (A.out_tokens) A.out_tokens[r] = token;
-      A.list_counts[r] = -1;
+__global__ __launch_bounds__(kLeftThreads) __attribute__((amdgpu_waves_per_eu(2))) void
+filter_left_kernel(FilterLaunch A) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  __shared__ unsigned long long left[kLeftThreads / kWave];
+  const long rows = (long)A.B * A.per_seq, step = gridDim.x;
+#pragma unroll 1
+  for (long base = blockIdx.x; base < rows; base += step * kLeftThreads) {
+    const long mine = base + threadIdx.x * step;
+    const unsigned long long mask = __ballot(mine < rows && A.list_counts[mine] == kGeneralRow);
+    if (lane_id() == 0) left[threadIdx.x / kWave] = mask;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < kLeftThreads / kWave; ++w) {
+#pragma unroll 1
+      for (unsigned long long m = uniform(left[w]); m; m &= m - 1) {
+        const int i = w * kWave + __ffsll((long long)m) - 1;
+        filter_one_row<LT, kLeftThreads, false, true>(A, base + i * step, lds);
+        __syncthreads();
+      }
     }
-    if (A.out_probs) write_probs<LT, THREADS>(row, V, f, A.out_probs + r * V);
+    __syncthreads();
   }
 }
 
@@ -1788,17 +1786,19 @@ struct FilterWorkspace {
   }
 };
 
-template <typename LT, int THREADS, bool PRE, bool GENERAL>
-void launch_rows(FilterLaunch L, hipStream_t stream) {
+// The LDS of a workgroup that takes rows, and its list's length: as much as 64 KB
+// hold where it also does the general path.
+template <int THREADS, bool GENERAL>
+size_t row_lds(FilterLaunch& L) {
   const size_t tiles = (L.V + kRowTile - 1) / kRowTile;
   const size_t keys = tiles * (kRowTile / 8) / L.group_octets * sizeof(uint16_t);
-  // few rows: as long a list as 64 KB of LDS hold
-  const size_t fixed = sizeof(RowShared<THREADS>) + keys;
-  L.list_cap = kCand;
-  if (few_rows((long)L.B * L.per_seq))
-    L.list_cap = (int)std::min((size_t)kCandFew, (65536 - fixed) / sizeof(unsigned long long));
-  const size_t lds = std::max(fixed + L.list_cap * sizeof(unsigned long long),
-                              GENERAL ? sizeof(FilterShared<THREADS>) : 0);
+  const size_t fixed = sizeof(RowShared<THREADS>) + keys, entry = sizeof(unsigned long long);
+  L.list_cap = GENERAL ? (int)std::min((size_t)kCandFew, (65024 - fixed) / entry) : kCand;
+  return std::max(fixed + L.list_cap * entry, GENERAL ? sizeof(FilterShared<THREADS>) : 0);
+}
+template <typename LT, int THREADS, bool PRE, bool GENERAL>
+void launch_rows(FilterLaunch L, hipStream_t stream) {
+  const size_t lds = row_lds<THREADS, GENERAL>(L);
   filter_rows_kernel<LT, THREADS, PRE, GENERAL>
       <<<dim3((unsigned)((long)L.B * L.per_seq)), THREADS, lds, stream>>>(L);
 }
@@ -1826,7 +1826,8 @@ hipError_t launch_filter(FilterLaunch L, hipStream_t stream) {
   // every token of a short row fits the list
   if (e == hipSuccess && !few_rows(rows) && L.V > kCand) {
     trace_before(stream, SV_KERNEL_FILTER_ROWS);
-    filter_general_kernel<LT><<<dim3(256), kGeneralThreads, 0, stream>>>(L);
+    const size_t lds = row_lds<kLeftThreads, true>(L);
+    filter_left_kernel<LT><<<dim3((unsigned)std::min(rows, 512L)), kLeftThreads, lds, stream>>>(L);
     trace_after(stream, SV_KERNEL_FILTER_ROWS);
     e = hipGetLastError();
   }
