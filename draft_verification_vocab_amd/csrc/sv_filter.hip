@@ -1753,7 +1753,11 @@ __global__ __launch_bounds__(kVerifyThreads) void residual_kernel(FilteredVerify
 namespace {
 
 // Few rows take workgroups of 512 threads; where they are long, their stream
-// gets a kernel of its own, spread over all CUs.
+// gets a kernel of its own, spread over all CUs.  For rows of 151936 in bf16 and
+// the one kind against the other: 513 rows 68 against 54 us under top-k, 85
+// against 152 with top-p in half of them, 85 against 109 without a filter; 1024
+// rows 111 against 79, 180 against 195, 144 against 146; 2048 rows 220 against 143,
+// 347 against 249, 277 against 253.
 bool few_rows(long rows) { return rows <= 512; }
 bool streams_apart(long rows, int V) { return few_rows(rows) && V > 16 * kRowTile; }
 
